@@ -76,6 +76,9 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 #define GDN_DEV_ERR_PATH 4   /* path entry outside [0, T) or not a child of the previous */
 #define GDN_DEV_ERR_TOKEN 8  /* draft token outside [0, V) (sampling acceptance) */
 #define GDN_DEV_ERR_NAN 16   /* a logits row holds a NaN (greedy acceptance) */
+#define GDN_DEV_ERR_LENGTH 32 /* q_start or seq_len malformed, or more tokens than T or the block table hold */
+#define GDN_DEV_ERR_PAGE 64   /* page or slot outside the pool */
+#define GDN_DEV_ERR_NO_PAGES 128 /* the pool has too few free pages, or a page count is out of range */
 
 typedef struct {
   int32_t n_layers;    /* L: leading dimension of every per-layer tensor */
@@ -360,6 +363,154 @@ gdn_status gdn_tape_rollback(const gdn_shape* shape, int32_t T, float* S, const 
 gdn_status gdn_conv_state_rollback(const gdn_shape* shape, int32_t T, void* conv_state,
                                    const void* x, const int32_t* path, const int32_t* n_keep,
                                    int32_t* win_idx, int32_t* dev_err, void* stream);
+
+/*
+ * ---- Attention layers of a hybrid stack: the paged key/value cache ----
+ *
+ * A hybrid stack interleaves GDN layers with full-attention layers (GDN page
+ * s2.1: one layer in four).  A round takes the same drafted tokens through
+ * both.  For the attention layers that is
+ *   kv_reserve   pages and slots for every sequence's new tokens,
+ *   kv_append    each layer's keys and values into those slots,
+ *   attn_verify  the new tokens' attention over everything cached and over
+ *                themselves, as a chain or along the draft tree,
+ *   kv_commit    once the accepted lengths (and paths) are known: the kept
+ *                path in place, the lengths moved on, unused pages given back.
+ * As in a GDN round nothing here waits for the host: lengths, block tables,
+ * slots and the free-page stack stay in device memory.  A plain decode step is
+ * a round with T = 1, and a prompt (or a chunk of one) is a round whose tokens
+ * are all kept.
+ *
+ * Sequences are either uniform, T new tokens each ([B,T,...], q_start NULL,
+ * n_tokens >= B*T), or packed: sequence b's new tokens are rows q_start[b] ..
+ * q_start[b+1]-1 of n_tokens, at most T of them and possibly none.  Rows
+ * behind the last sequence are never read or written (kv_reserve gives them
+ * slot -1).
+ *
+ * Caches (dtype as k and v), per layer:
+ *   k_cache [L,P,Hkv,page,Dk]       a token's key in one piece
+ *   v_cache [L,P,Hkv,page/8,D,8]    eight consecutive tokens of a channel in
+ *                                   one piece, the operand order of P V
+ * Slot s is place s % page of page s / page.
+ *
+ * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256;
+ * n_q_heads % n_kv_heads == 0; F32 or BF16; n_pages * page_size < 2^31;
+ * max_blocks * page_size <= 2^30; batch < 65536; n_layers * n_kv_heads <
+ * 65536; n_tokens <= 2^24.  A sequence whose lengths are malformed
+ * (q_start decreasing or outside [0, n_tokens], more than T new tokens,
+ * seq_len < 0, seq_len + new > max_blocks * page_size) sets
+ * GDN_DEV_ERR_LENGTH and is left out.
+ */
+typedef struct {
+  int32_t n_layers;   /* L: leading dimension of every per-layer tensor */
+  int32_t batch;      /* B: sequences */
+  int32_t n_q_heads;  /* Hq, multiple of Hkv; query head h reads key head h / (Hq/Hkv) */
+  int32_t n_kv_heads; /* Hkv */
+  int32_t head_dim;   /* D */
+  int32_t page_size;  /* tokens per page */
+  int32_t n_pages;    /* P: pages of the pool */
+  int32_t max_blocks; /* width of the block table */
+  int32_t dtype;      /* gdn_dtype of q, k, v, both caches and o */
+} kv_shape;
+
+/*
+ * Block tables and slots for the new tokens.
+ *   seq_len     [B] int32, tokens already cached; sequence b holds pages
+ *               block_table[b][0 .. ceil(seq_len/page)-1]
+ *   block_table [B,max_blocks] int32 in/out: receives the new pages behind
+ *               them; nothing else of it is written
+ *   free_pages  [P] int32: the stack of free pages, entries 0 .. n_free-1
+ *   n_free      [1] int32: pages free before;  n_left [1]: after.  They may
+ *               not be the same address; free_pages is not written, so until
+ *               kv_commit the same call gives the same answer
+ *   slots       [n_tokens] int32: the slot of every new token
+ * Pages are taken from the top of the stack in order of sequence, then of
+ * block.  A sequence is served while its pages and those of all sequences
+ * before it fit in n_free (one that needs none always is); the others get slot
+ * -1 everywhere, no page, and GDN_DEV_ERR_NO_PAGES.  A page number outside
+ * the pool gives slot -1 and GDN_DEV_ERR_PAGE.
+ */
+gdn_status kv_reserve(const kv_shape* shape, int32_t T, int32_t n_tokens, const int32_t* q_start,
+                      const int32_t* seq_len, int32_t* block_table, const int32_t* free_pages,
+                      const int32_t* n_free, int32_t* n_left, int32_t* slots, int32_t* dev_err,
+                      void* stream);
+
+/*
+ * Write L layers' new keys and values into their slots.
+ *   k, v  [L,n_tokens,Hkv,D] with k_ld (v_ld) elements from one token to the
+ *         next (>= Hkv*D and a multiple of 16 bytes; a layer takes n_tokens *
+ *         ld), so they may be slices of one projection's output
+ *   slots [n_tokens] int32 as kv_reserve gives them; -1 skips the token.  Any
+ *         other slot outside the pool skips it and sets GDN_DEV_ERR_PAGE.  Two
+ *         tokens of a call may not share a slot.
+ * k, v and the caches are 16-byte aligned.
+ */
+gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int64_t k_ld,
+                     const void* v, int64_t v_ld, const int32_t* slots, void* k_cache,
+                     void* v_cache, int32_t* dev_err, void* stream);
+
+/*
+ * Attention of the new tokens over the paged cache, into which kv_append has
+ * already written their own keys and values:
+ *   o = sum_j softmax_j(scale * q . k_j) v_j
+ * over the sequence's seq_len cached tokens and, of its new ones, the token
+ * itself and those before it (parent NULL: a chain) or its ancestors
+ * (parent: [n_tokens] int32 laid out as the tokens, node v's parent in
+ * [-1, v-1] within its sequence; T <= 64).
+ *   q           [L,n_tokens,Hq,D], q_ld elements between tokens (as k_ld)
+ *   o           [L,n_tokens,Hq,D] contiguous, dtype of q
+ *   seq_len     [B] int32: cached tokens before the new ones
+ *   block_table [B,max_blocks] as kv_reserve left it
+ *   scale       finite; 1/sqrt(D) in most models
+ *   workspace   device scratch of attn_verify_workspace_bytes(shape, T,
+ *               n_tokens), 16-byte aligned; calls that may overlap need one
+ *               each
+ * Scores, the softmax's running maximum and sum, and the output sums are fp32;
+ * with bf16 the probabilities are rounded to bf16 for the product with V.
+ * Cache places behind a sequence's last token may hold anything, NaN included.
+ * So may masked new tokens: an infinite or NaN value (or key) of a token
+ * reaches only the rows that attend to it.  A malformed parent array sets
+ * GDN_DEV_ERR_PARENT and leaves the sequence's rows of o unwritten.  A page
+ * number outside the pool sets GDN_DEV_ERR_PAGE; its tokens then count as
+ * masked, and the rows of that sequence are meaningless.  The result is the same bit for bit from call to call.
+ */
+gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const int32_t* q_start,
+                       const int32_t* seq_len, const int32_t* block_table, const int32_t* parent,
+                       const void* q, int64_t q_ld, float scale, const void* k_cache,
+                       const void* v_cache, void* o, void* workspace, size_t workspace_bytes,
+                       int32_t* dev_err, void* stream);
+
+/* Bytes of device workspace attn_verify needs (0 for arguments it refuses). */
+size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_tokens);
+
+/*
+ * The end of a round: n = n_keep[b] new tokens of every sequence stay.
+ *   path    [B,T] int32 or NULL (tokens 0 .. n-1): the accepted nodes, as
+ *           spec_accept_prefix writes them; T <= 64.  Token path[b][i]'s key
+ *           and value go to the slot of token i, from the round's k and v
+ *           (kv_append's inputs), so no cache row is read
+ *   done    [B] int32 or NULL: a sequence with done[b] != 0 ends, its length
+ *           becomes 0 and all of its pages go back
+ *   seq_len, block_table, slots   as kv_reserve took and left them
+ *   seq_len_out [B]: seq_len + n, or 0; may be seq_len itself
+ *   n_left  [1] as kv_reserve left it;  n_free [1]: pages free afterwards; may
+ *           be n_left itself
+ *   free_pages  [P]: receives the pages behind the kept tokens on top of its
+ *           n_left entries, in order of sequence, then of block
+ * n_keep outside [0, new tokens] sets GDN_DEV_ERR_N_KEEP and a path entry
+ * outside them GDN_DEV_ERR_PATH; of such a sequence nothing is kept.  Nothing
+ * is kept or given back of a sequence that kv_reserve did not serve (first
+ * slot -1); n_keep > 0 then sets GDN_DEV_ERR_NO_PAGES.  With path NULL, k, v
+ * and the caches are not used and may be NULL.
+ * Source: GDN page s4 (the window rebuilt from the accepted raw tokens), for
+ * the attention layers' cache.
+ */
+gdn_status kv_commit(const kv_shape* shape, int32_t T, int32_t n_tokens, const int32_t* q_start,
+                     const int32_t* path, const int32_t* n_keep, const int32_t* done,
+                     const int32_t* slots, const int32_t* seq_len, int32_t* seq_len_out,
+                     const int32_t* block_table, int32_t* free_pages, const int32_t* n_left,
+                     int32_t* n_free, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                     void* k_cache, void* v_cache, int32_t* dev_err, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* gdn_status_string(int32_t status);

@@ -8,7 +8,9 @@ no CPU fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -23,6 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libgdnverify.so")
 ACCEPT_SCRATCH_BYTES = 1 << 20  # GDN_ACCEPT_SCRATCH_BYTES
 GDN_F32, GDN_BF16 = 0, 1
 DEV_ERR_N_KEEP, DEV_ERR_PARENT, DEV_ERR_PATH, DEV_ERR_TOKEN, DEV_ERR_NAN = 1, 2, 4, 8, 16
+DEV_ERR_LENGTH, DEV_ERR_PAGE, DEV_ERR_NO_PAGES = 32, 64, 128
 
 EXPORTS = ("gdn_verify_chunk", "gdn_verify_chunk_replay", "gdn_tree_verify",
            "gdn_tree_verify_replay", "spec_accept_prefix", "spec_accept_prefix_noalloc",
@@ -30,7 +33,8 @@ EXPORTS = ("gdn_verify_chunk", "gdn_verify_chunk_replay", "gdn_tree_verify",
            "spec_sample_workspace_bytes", "gdn_prefill", "gdn_prefill_workspace_bytes",
            "gdn_round_rollback",
            "spec_accept_workspace_bytes", "gdn_tape_rollback", "gdn_conv_state_rollback",
-           "gdn_status_string", "gdn_abi_version")
+           "gdn_status_string", "gdn_abi_version",
+           "kv_reserve", "kv_append", "attn_verify", "attn_verify_workspace_bytes", "kv_commit")
 
 
 class GdnError(RuntimeError):
@@ -85,6 +89,41 @@ class GdnShape:
                 else (self.L, self.B, T, self.Hv))
 
 
+class _CKvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_layers", "batch", "n_q_heads", "n_kv_heads", "head_dim", "page_size",
+                 "n_pages", "max_blocks", "dtype")]
+
+
+@dataclass(frozen=True)
+class KvShape:
+    """Mirror of kv_shape: the attention layers' heads, and their page pool."""
+    L: int
+    B: int
+    Hq: int
+    Hkv: int
+    D: int
+    page: int
+    n_pages: int
+    max_blocks: int
+    dtype: torch.dtype = torch.bfloat16
+
+    @functools.cached_property
+    def c(self) -> _CKvShape:
+        if self.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("cache dtype must be float32 or bfloat16")
+        return _CKvShape(self.L, self.B, self.Hq, self.Hkv, self.D, self.page, self.n_pages,
+                         self.max_blocks, GDN_BF16 if self.dtype == torch.bfloat16 else GDN_F32)
+
+    @property
+    def k_cache_shape(self) -> tuple:
+        return (self.L, self.n_pages, self.Hkv, self.page, self.D)
+
+    @property
+    def v_cache_shape(self) -> tuple:
+        return (self.L, self.n_pages, self.Hkv, self.page // 8, self.D, 8)
+
+
 _lib = None
 
 
@@ -120,11 +159,20 @@ def lib() -> ctypes.CDLL:
         L.gdn_status_string.argtypes = [I32]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []
+        KP, I64 = ctypes.POINTER(_CKvShape), ctypes.c_int64
+        L.kv_reserve.argtypes = [KP, I32, I32, P, P, P, P, P, P, P, P, P]
+        L.kv_append.argtypes = [KP, I32, P, I64, P, I64, P, P, P, P, P]
+        L.attn_verify.argtypes = [KP, I32, I32, P, P, P, P, P, I64, ctypes.c_float, P, P, P, P, SZ,
+                                  P, P]
+        L.attn_verify_workspace_bytes.argtypes = [KP, I32, I32]
+        L.attn_verify_workspace_bytes.restype = SZ
+        L.kv_commit.argtypes = [KP, I32, I32] + [P] * 11 + [P, I64, P, I64, P, P, P, P]
         for name in ("gdn_verify_chunk", "gdn_verify_chunk_replay", "gdn_tree_verify",
                      "gdn_tree_verify_replay", "spec_accept_prefix",
                      "spec_accept_prefix_noalloc", "spec_accept_sample",
                      "gdn_prefill", "gdn_round_rollback",
-                     "gdn_tape_rollback", "gdn_conv_state_rollback", "gdn_abi_version"):
+                     "gdn_tape_rollback", "gdn_conv_state_rollback", "gdn_abi_version",
+                     "kv_reserve", "kv_append", "attn_verify", "kv_commit"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -429,3 +477,136 @@ def gdn_conv_state_rollback(sh: GdnShape, conv_state, x, n_keep, path=None, win_
     _dev(conv_state.device, x, n_keep, path, win_idx, dev_err)
     _check(lib().gdn_conv_state_rollback(ctypes.byref(sh.c()), T, cp, xp, pp, np_, wp, de,
                                          _stream(stream)), "gdn_conv_state_rollback")
+
+
+# ---- attention layers: paged key/value cache and attention over it ----
+
+def _on(device):
+    """The device of the call's tensors, made current where it is not."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape):
+    """Pointer and row stride of a [L,N,H,D] tensor whose token rows may be a
+    slice of wider ones."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    L, N, H, D = shape
+    st = t.stride()
+    ld = st[1] if N > 1 else st[0] if L > 1 else H * D
+    if (st[3] != 1 or (H > 1 and st[2] != D) or ld < H * D or (L > 1 and st[0] != N * ld)
+            or ld * t.element_size() % 16):
+        raise ValueError("%s: heads must be contiguous, rows a multiple of 16 bytes apart and "
+                         "layers N rows apart (strides %s)" % (name, st))
+    if t.data_ptr() % 16:
+        raise ValueError("%s must be 16-byte aligned" % name)
+    return t.data_ptr(), ld
+
+
+def _caches(sh: KvShape, k_cache, v_cache):
+    return (_need(k_cache, "k_cache", sh.dtype, sh.k_cache_shape),
+            _need(v_cache, "v_cache", sh.dtype, sh.v_cache_shape))
+
+
+def _starts(sh: KvShape, q_start):
+    return _opt(q_start, "q_start", torch.int32, (sh.B + 1,))
+
+
+def kv_reserve(sh: KvShape, seq_len, block_table, free_pages, n_free, n_left, slots, T: int,
+               q_start=None, dev_err=None, stream=None):
+    """Pages and slots for every sequence's new tokens (T each, or rows
+    q_start[b] .. q_start[b+1]-1 of the slots)."""
+    i32 = torch.int32
+    N = int(slots.shape[0])
+    args = [_starts(sh, q_start), _need(seq_len, "seq_len", i32, (sh.B,), 4),
+            _need(block_table, "block_table", i32, (sh.B, sh.max_blocks), 4),
+            _need(free_pages, "free_pages", i32, (sh.n_pages,), 4),
+            _need(n_free, "n_free", i32, (1,), 4), _need(n_left, "n_left", i32, (1,), 4),
+            _need(slots, "slots", i32, (N,), 4), _opt(dev_err, "dev_err", i32, (1,))]
+    dev = seq_len.device
+    _dev(dev, q_start, block_table, free_pages, n_free, n_left, slots, dev_err)
+    with _on(dev):
+        _check(lib().kv_reserve(ctypes.byref(sh.c), T, N, *args, _stream(stream)), "kv_reserve")
+
+
+def kv_append(sh: KvShape, k, v, slots, k_cache, v_cache, dev_err=None, stream=None):
+    """Write k and v [L,N,Hkv,D] into their slots [N]."""
+    N = int(slots.shape[0])
+    kp, kl = _rows(k, "k", sh.dtype, (sh.L, N, sh.Hkv, sh.D))
+    vp, vl = _rows(v, "v", sh.dtype, (sh.L, N, sh.Hkv, sh.D))
+    sp = _need(slots, "slots", torch.int32, (N,), 4)
+    kc, vc = _caches(sh, k_cache, v_cache)
+    de = _opt(dev_err, "dev_err", torch.int32, (1,))
+    dev = k.device
+    _dev(dev, v, slots, k_cache, v_cache, dev_err)
+    with _on(dev):
+        _check(lib().kv_append(ctypes.byref(sh.c), N, kp, kl, vp, vl, sp, kc, vc, de,
+                               _stream(stream)), "kv_append")
+
+
+def attn_verify_workspace_bytes(sh: KvShape, T: int, n_tokens: int) -> int:
+    return int(lib().attn_verify_workspace_bytes(ctypes.byref(sh.c), T, n_tokens))
+
+
+def attn_verify(sh: KvShape, q, seq_len, block_table, k_cache, v_cache, o, workspace, T: int,
+                q_start=None, parent=None, scale: Optional[float] = None, dev_err=None,
+                stream=None):
+    """Attention of the new tokens q [L,N,Hq,D] over the cache, their own keys
+    and values included: a chain, or along the tree of parent [N].  scale is
+    1/sqrt(D) unless given."""
+    N = int(q.shape[1])
+    i32 = torch.int32
+    qp, ql = _rows(q, "q", sh.dtype, (sh.L, N, sh.Hq, sh.D))
+    op = _need(o, "o", sh.dtype, (sh.L, N, sh.Hq, sh.D))
+    kc, vc = _caches(sh, k_cache, v_cache)
+    if (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8
+            or not workspace.is_cuda or not workspace.is_contiguous()
+            or workspace.data_ptr() % 16):
+        raise ValueError("workspace must be a 16-byte aligned device uint8 tensor")
+    args = [_starts(sh, q_start), _need(seq_len, "seq_len", i32, (sh.B,), 4),
+            _need(block_table, "block_table", i32, (sh.B, sh.max_blocks), 4),
+            _opt(parent, "parent", i32, (N,))]
+    de = _opt(dev_err, "dev_err", i32, (1,))
+    dev = q.device
+    _dev(dev, q_start, seq_len, block_table, parent, k_cache, v_cache, o, workspace, dev_err)
+    with _on(dev):
+        _check(lib().attn_verify(ctypes.byref(sh.c), T, N, *args, qp, ql,
+                                 sh.D ** -0.5 if scale is None else float(scale), kc, vc, op,
+                                 workspace.data_ptr(), workspace.numel(), de, _stream(stream)),
+               "attn_verify")
+
+
+def kv_commit(sh: KvShape, k, v, slots, n_keep, seq_len, seq_len_out, block_table, free_pages,
+              n_left, n_free, k_cache, v_cache, T: int, q_start=None, path=None, done=None,
+              dev_err=None, stream=None):
+    """Keep n_keep[b] new tokens of every sequence (those of path [B,T], or the
+    first ones), move the lengths on and give unused pages back.  Without a
+    path k, v and the caches are not used."""
+    i32 = torch.int32
+    N = int(slots.shape[0])
+    kv = [None, 0, None, 0, None, None]
+    if path is not None:
+        kv = [*_rows(k, "k", sh.dtype, (sh.L, N, sh.Hkv, sh.D)),
+              *_rows(v, "v", sh.dtype, (sh.L, N, sh.Hkv, sh.D)), *_caches(sh, k_cache, v_cache)]
+    args = [_starts(sh, q_start), _opt(path, "path", i32, (sh.B, T)),
+            _need(n_keep, "n_keep", i32, (sh.B,), 4), _opt(done, "done", i32, (sh.B,)),
+            _need(slots, "slots", i32, (N,), 4), _need(seq_len, "seq_len", i32, (sh.B,), 4),
+            _need(seq_len_out, "seq_len_out", i32, (sh.B,), 4),
+            _need(block_table, "block_table", i32, (sh.B, sh.max_blocks), 4),
+            _need(free_pages, "free_pages", i32, (sh.n_pages,), 4),
+            _need(n_left, "n_left", i32, (1,), 4), _need(n_free, "n_free", i32, (1,), 4)]
+    de = _opt(dev_err, "dev_err", i32, (1,))
+    dev = slots.device
+    _dev(dev, q_start, path, n_keep, done, seq_len, seq_len_out, block_table, free_pages, n_left,
+         n_free, dev_err, *((k, v, k_cache, v_cache) if path is not None else ()))
+    with _on(dev):
+        _check(lib().kv_commit(ctypes.byref(sh.c), T, N, *args, *kv, de, _stream(stream)),
+               "kv_commit")
