@@ -395,8 +395,9 @@ gdn_status gdn_conv_state_rollback(const gdn_shape* shape, int32_t T, void* conv
  *
  * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256;
  * n_q_heads % n_kv_heads == 0; F32 or BF16; n_pages * page_size < 2^31;
- * max_blocks * page_size <= 2^30; batch < 65536; n_layers * n_kv_heads <
- * 65536; n_tokens <= 2^24.  A sequence whose lengths are malformed
+ * max_blocks * page_size <= 2^30; batch < 65536; n_q_heads < 65536; n_layers *
+ * n_kv_heads < 65536; n_layers * batch <= 2^23; n_tokens <= 2^24, and for
+ * attn_verify n_tokens * n_q_heads / n_kv_heads <= 2^30.  A sequence whose lengths are malformed
  * (q_start decreasing or outside [0, n_tokens], more than T new tokens,
  * seq_len < 0, seq_len + new > max_blocks * page_size) sets
  * GDN_DEV_ERR_LENGTH and is left out.

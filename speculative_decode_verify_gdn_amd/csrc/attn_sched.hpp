@@ -28,11 +28,11 @@ struct AttnSched {
 // A shared item as its first workgroup describes it for the join: last = -1 if
 // there is none.
 struct AttnJoin {
-  int last;        // last workgroup with a fragment
-  int rows;        // rows of the tile
-  int row0;        // first row of the tile within the sequence's rows
-  int tok0;        // first token of the sequence
-  int layer, head;
+  int last;  // last workgroup with a fragment
+  int rows;  // rows of the tile
+  int skip;  // the tile's first row within its first token
+  int pad;
+  long long out;  // of that token's first query head of the tile's key head, in o
 };
 
 // One item, and where it lies.
@@ -44,18 +44,20 @@ struct AttnItem {
 
 template <int R>
 struct AttnLine {
-  // Cost of the first i tiles of one head: with c = ctx + kItemCost,
-  // sum over tiles of (c + tokens up to the tile's end).
-  static __device__ __forceinline__ long long upto(const KvSpan& r, int G, int i) {
+  // Cost of the first i tiles of one head: a tile costs its cached tokens, the
+  // new ones up to its end at `per` a tile, and kItemCost.
+  static __device__ __forceinline__ long long upto(const KvSpan& r, int per, int i) {
     return static_cast<long long>(i) * (r.ctx + kItemCost) +
-           static_cast<long long>(R) * i * (i + 1) / (2 * G);
+           ((static_cast<long long>(i) * (i + 1) * per) >> 1);
   }
   static __device__ __forceinline__ int tiles(const KvSpan& r, int G) {
-    return static_cast<int>((static_cast<long long>(r.n) * G + R - 1) / R);
+    return (r.n * G + R - 1) / R;  // n * G <= 2^30
   }
   static __device__ __forceinline__ long long sequence(const KvSpan& r, int G, int H) {
-    return H * upto(r, G, tiles(r, G));
+    return H * upto(r, per(G), tiles(r, G));
   }
+  // tokens of a tile, at least one
+  static __device__ __forceinline__ int per(int G) { return G >= R ? 1 : R / G; }
 };
 
 // a * b / c, rounded the same way for everyone who asks: monotone in a, 0 at
@@ -66,120 +68,130 @@ __device__ __forceinline__ long long part_of(long long a, long long b, long long
                                 static_cast<double>(c));
 }
 
-template <int NT>
-__device__ __forceinline__ long long sched_scan(long long v, long long* lds, long long& total) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const long long o = __shfl_up(v, off, kWave);
-    if (lane >= off) v += o;
-  }
-  __syncthreads();
-  if (lane == kWave - 1) lds[wave] = v;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < NT / kWave; ++w) {
-    if (w < wave) before += lds[w];
-    total += lds[w];
-  }
-  return v + before;
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long long lane_of(long long x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(x), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), lane);
+  return static_cast<long long>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ long long uni(long long x) { return lane_of(x, 0); }
+
+// v plus the v of the lanes that DPP control C (row mask M) takes it from.
+template <int C, int M>
+__device__ __forceinline__ long long dpp_add(long long v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), C, M, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), C, M, 0xf, false);
+  return v + static_cast<long long>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Inclusive prefix sum over a wave: within rows of 16, then rows 0 and 2 into
+// 1 and 3, then the first half into the second.
+__device__ __forceinline__ long long wave_scan(long long v) {
+  v = dpp_add<0x111, 0xf>(v);
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);
+  return dpp_add<0x143, 0xc>(v);
 }
 
 // The line's length, and the sequence and place where this workgroup's part
-// begins.  lds: NT/64 + 2 long longs.  Every thread returns the same values.
+// begins, found by every wave for itself (64 sequences a step, no barrier: what
+// a call of few keys waits for is this chain of latencies).  Uniform.
 struct AttnStart {
   AttnSched s;
   long long lo, hi;  // this workgroup's part; empty if it has none
   int layer, b;      // of the first item
   long long seq_at;  // where sequence b begins
+  KvSpan span;       // of sequence b
 };
 
-template <int R, int NT>
-__device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long long grain,
-                                long long* lds) {
+template <int R>
+__device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long long grain) {
   const KvBatch& k = p.k;
-  const int tid = threadIdx.x;
-  long long* found = lds + NT / kWave;
+  const int lane = threadIdx.x % kWave;
   long long sum = 0, v = 0, upto = 0;
+  KvSpan r{};
   bool bad = false;
-  for (int c = 0; c < k.B; c += NT) {
+  auto step = [&](int c) {
     v = 0;
-    if (c + tid < k.B) {
-      const KvSpan r = kv_span(k, c + tid);
+    if (c + lane < k.B) {
+      r = kv_span(k, c + lane);
       bad |= !r.ok;
       v = AttnLine<R>::sequence(r, G, p.Hkv);
     }
-    long long total;
-    upto = sum + sched_scan<NT>(v, lds, total);
-    sum += total;
+    upto = wave_scan(v);
+  };
+  for (int c = 0; c < k.B; c += kWave) {
+    step(c);
+    upto += sum;
+    sum = lane_of(upto, kWave - 1);
   }
-  if (bad && wg == 0 && p.dev_err) atomicOr(p.dev_err, GDN_DEV_ERR_LENGTH);
-  AttnStart a;
+  if (wg == 0 && __any(bad) && threadIdx.x == 0 && p.dev_err)
+    atomicOr(p.dev_err, GDN_DEV_ERR_LENGTH);
+  AttnStart a{};
   a.s.layer = sum;
   a.s.total = sum * p.L;
-  const long long want = (a.s.total + grain - 1) / grain;
-  a.s.active = static_cast<int>(want < n_wg ? want : n_wg);
-  a.lo = a.hi = 0;
-  a.layer = a.b = 0;
-  a.seq_at = 0;
+  const long long most = static_cast<long long>(n_wg) * grain;
+  a.s.active = a.s.total >= most
+                   ? n_wg
+                   : static_cast<int>((static_cast<double>(a.s.total) + grain - 1) / grain);
+  a.s.active = uni(a.s.active);
   if (wg >= a.s.active) return a;
-  a.lo = part_of(wg, a.s.total, a.s.active);
-  a.hi = part_of(wg + 1, a.s.total, a.s.active);
-  a.layer = static_cast<int>(a.lo / sum);
+  a.lo = uni(part_of(wg, a.s.total, a.s.active));
+  a.hi = uni(part_of(wg + 1, a.s.total, a.s.active));
+  a.layer = p.L == 1 ? 0 : static_cast<int>(a.lo / sum);
   const long long x = a.lo - a.layer * sum;
-  if (k.B <= NT) {  // the one chunk is still in registers
-    if (upto - v <= x && x < upto) {
-      found[0] = tid;
-      found[1] = upto - v;
+  long long before = 0;
+  for (int c = 0;; c += kWave) {
+    if (k.B > kWave) {  // one step's values are still in registers
+      step(c);
+      upto += before;
+      before = lane_of(upto, kWave - 1);
     }
-  } else {
-    long long before = 0;
-    for (int c = 0; c < k.B; c += NT) {
-      v = 0;
-      if (c + tid < k.B) v = AttnLine<R>::sequence(kv_span(k, c + tid), G, p.Hkv);
-      long long total;
-      upto = before + sched_scan<NT>(v, lds, total);
-      if (upto - v <= x && x < upto) {
-        found[0] = c + tid;
-        found[1] = upto - v;
-      }
-      before += total;
+    const unsigned long long who = __ballot(upto - v <= x && x < upto);
+    if (who || c + kWave >= k.B) {
+      const int at = who ? __builtin_ctzll(who) : 0;
+      a.b = c + at;
+      a.seq_at = a.layer * sum + lane_of(upto - v, at);
+      a.span.s = __builtin_amdgcn_readlane(r.s, at);
+      a.span.n = __builtin_amdgcn_readlane(r.n, at);
+      a.span.ctx = __builtin_amdgcn_readlane(r.ctx, at);
+      a.span.ok = true;
+      return a;
     }
   }
-  __syncthreads();
-  a.b = static_cast<int>(found[0]);
-  a.seq_at = a.layer * sum + found[1];
-  return a;
 }
 
 // The item at place x of the line, x within the sequence (layer, b) that begins
 // at seq_at.
 template <int R>
-__device__ AttnItem attn_item(const AttnArgs& p, int G, int layer, int b, long long seq_at,
-                              long long x) {
+__device__ AttnItem attn_item(const AttnArgs& p, int G, int layer, int b, const KvSpan& span,
+                              long long seq_at, long long x) {
   AttnItem it;
   it.layer = layer;
   it.b = b;
-  it.span = kv_span(p.k, b);
-  const int nt = AttnLine<R>::tiles(it.span, G);
-  const long long head = AttnLine<R>::upto(it.span, G, nt);
+  it.span = span;
+  const int nt = AttnLine<R>::tiles(span, G), per = AttnLine<R>::per(G);
+  const long long head = AttnLine<R>::upto(span, per, nt);
   const long long off = x - seq_at;
-  it.h = static_cast<int>(off / head);
-  const long long in = off - it.h * head;
+  int h = p.Hkv == 1 ? 0
+                     : uni(static_cast<int>(static_cast<double>(off) / static_cast<double>(head)));
+  if (h * head > off) --h;
+  if ((h + 1) * head <= off) ++h;
+  it.h = h;
+  const long long in = off - h * head;
   int lo = 0, hi = nt - 1;  // the last tile that begins at or before `in`
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (AttnLine<R>::upto(it.span, G, mid) <= in)
+    if (AttnLine<R>::upto(span, per, mid) <= in)
       lo = mid;
     else
       hi = mid - 1;
   }
   it.tile = lo;
-  const long long a = AttnLine<R>::upto(it.span, G, lo);
-  it.at = seq_at + it.h * head + a;
-  it.cost = AttnLine<R>::upto(it.span, G, lo + 1) - a;
+  const long long a = AttnLine<R>::upto(span, per, lo);
+  it.at = seq_at + h * head + a;
+  it.cost = AttnLine<R>::upto(span, per, lo + 1) - a;
   return it;
 }
 

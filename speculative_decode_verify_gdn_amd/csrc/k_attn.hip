@@ -27,6 +27,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 8.f;
 
 // ---- element types: 32 keys of K and V as MFMA operands
 
@@ -44,6 +45,17 @@ struct Frag<uint16_t> {
   typedef bf16x8 K;                 // 8 channels of a key
   typedef bf16x8 V;                 // 8 keys of a channel
   static constexpr int kVLoads = 1;
+  // An exponent of all ones, plus one in its last place, carries into the sign.
+  static constexpr uint32_t kExp = 0x7f807f80u, kOne = 0x00800080u, kTop = 0x80008000u;
+  static __device__ __forceinline__ uint32_t spread(uint32_t top) { return (top >> 15) * 0xffffu; }
+  // The words of 8 keys of which the bits say which to keep.
+  static __device__ __forceinline__ u32x4 keep(uint32_t there) {
+    u32x4 m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m[j] = ((there >> (2 * j)) & 1) * 0xffffu + ((there >> (2 * j + 1)) & 1) * 0xffff0000u;
+    return m;
+  }
   static __device__ __forceinline__ int key_of(int t, int g, int i) { return 8 * g + 4 * t + i; }
   // the key whose row lane c feeds to tile t
   static __device__ __forceinline__ int row_key(int t, int c) {
@@ -64,6 +76,14 @@ struct Frag<float> {
   typedef floatx4 K;
   typedef floatx4 V;
   static constexpr int kVLoads = 2;
+  static constexpr uint32_t kExp = 0x7f800000u, kOne = 0x00800000u, kTop = 0x80000000u;
+  static __device__ __forceinline__ uint32_t spread(uint32_t top) { return (top >> 31) * ~0u; }
+  static __device__ __forceinline__ u32x4 keep(uint32_t there) {
+    u32x4 m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = ((there >> j) & 1) * ~0u;
+    return m;
+  }
   static __device__ __forceinline__ int key_of(int t, int g, int i) { return 16 * t + 4 * g + i; }
   static __device__ __forceinline__ int row_key(int t, int c) { return 16 * t + c; }
   static __device__ __forceinline__ floatx4 score(K k, K q, floatx4 s) {
@@ -93,25 +113,36 @@ __device__ __forceinline__ floatx4 weigh(const floatx4* v, const floatx4* p, flo
   return o;
 }
 
-__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
-__device__ __forceinline__ uint32_t bits(__bf16 x) {
-  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, x)) << 16;
+__device__ __forceinline__ bool not_finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
 }
-__device__ __forceinline__ bool not_finite(uint32_t b) { return (b & 0x7f800000u) == 0x7f800000u; }
 
 __device__ __forceinline__ uint16_t to_out(float x, uint16_t) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
 __device__ __forceinline__ float to_out(float x, float) { return x; }
 
-// Maximum over the four lanes that hold a row's keys (c, c+16, c+32, c+48).
+// Over the four lanes that hold a row's keys (c, c+16, c+32, c+48): halves
+// exchanged, then rows of 16.
+__device__ __forceinline__ floatx2 swap32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return floatx2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ floatx2 swap16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return floatx2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
 __device__ __forceinline__ float row_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16, kWave));
-  return fmaxf(x, __shfl_xor(x, 32, kWave));
+  const floatx2 a = swap32(x);
+  const floatx2 b = swap16(fmaxf(a[0], a[1]));
+  return fmaxf(b[0], b[1]);
 }
 __device__ __forceinline__ float row_sum(float x) {
-  x += __shfl_xor(x, 16, kWave);
-  return x + __shfl_xor(x, 32, kWave);
+  const floatx2 a = swap32(x);
+  const floatx2 b = swap16(a[0] + a[1]);
+  return b[0] + b[1];
 }
 
 // Ancestors (and self) of every node of a sequence's tree, as bits; false if
@@ -160,6 +191,24 @@ struct Places {
   }
 };
 
+// What a row sees of `count` consecutive keys from `base` on, as bits: in a
+// chain the keys below lim; in a tree the cached ones (below ctx) and those of
+// its ancestors, whose bits `mask` holds from ctx on.
+__device__ __forceinline__ uint32_t chain_sees(int lim, int base, int count) {
+  return (1u << min(max(lim - base, 0), count)) - 1u;
+}
+__device__ __forceinline__ uint32_t tree_sees(uint64_t mask, int ctx, int base, int count) {
+  const int in = base - ctx;  // place among the new tokens
+  uint64_t m = in >= 64 ? 0 : in >= 0 ? mask >> in : in <= -32 ? ~0ull : ~(~mask << -in);
+  return static_cast<uint32_t>(m) & ((1u << count) - 1u);
+}
+
+// Token of row `row` of a tile that begins `skip` rows into token 0 of it, with
+// inv = 1/G: exact for the small numbers at hand (skip + row < 2^17).
+__device__ __forceinline__ int tile_token(int skip, int row, float inv) {
+  return static_cast<int>((static_cast<float>(skip + row) + 0.5f) * inv);
+}
+
 // ---- few query rows: the waves of a workgroup take different keys
 //
 // R = 16 NT rows; each wave streams 32 keys at a time straight from the cache
@@ -173,11 +222,13 @@ struct Stream {
   static constexpr int QLD = D + Frag<T>::kPad;
   static constexpr int kC = D < 128 ? D : 128;  // channels joined at a time
   struct Lds {
-    T q[R * QLD];
-    float join[W][16][kC + 4];
-    float m[W][R], l[W][R];
+    union {  // one after the other
+      T q[R * QLD];
+      float join[W][R][kC + 4];
+    };
+    float m[W][R], l[W][R], inv[R];
     TreeLds tree;
-    long long scan[W + 2];
+    int any_odd;
   };
 };
 
@@ -188,19 +239,21 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
   constexpr int W = St::W, R = St::R, QLD = St::QLD;
   constexpr int KJ = D / F::kPerK;  // score products per tile
   constexpr int MT = D / 16;        // output tiles
+  constexpr int VE = 16 / sizeof(T);  // keys of a V operand
   __shared__ typename St::Lds sh;
   const KvBatch& k = p.k;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, g = lane / 16;
   const int G = p.Hq / p.Hkv;
+  const float inv_g = 1.f / static_cast<float>(G);
   const int wg = blockIdx.x;
   const Places<R, D> places(p.ws, n_wg);
-  const AttnStart st = attn_start<R, W * kWave>(p, G, wg, n_wg, grain, sh.scan);
+  const AttnStart st = attn_start<R>(p, G, wg, n_wg, grain);
   AttnJoin join;
   join.last = -1;
-  const float sgn = p.scale < 0.f ? -1.f : 1.f;
-  // scores are compared unscaled; at least the smallest normal, so that a
-  // masked -inf stays -inf at scale 0
+  // scores are compared unscaled (a negative scale turns q's sign); at least
+  // the smallest normal, so that a masked -inf stays -inf at scale 0
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
   const int ps = 1 << k.page_shift;
   const size_t head_sz = static_cast<size_t>(ps) * D;
@@ -208,80 +261,29 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 
   long long x = st.lo, seq_at = st.seq_at;
   int layer = st.layer, b = st.b;
+  KvSpan r = st.span;
   while (x < st.hi) {
-    const AttnItem it = attn_item<R>(p, G, layer, b, seq_at, x);
-    const KvSpan& r = it.span;
+    const AttnItem it = attn_item<R>(p, G, layer, b, r, seq_at, x);
     const long long end = it.at + it.cost;
     const long long till = end < st.hi ? end : st.hi;
-    const int rows_all = r.n * G;
     const int row0 = it.tile * R;
-    const int rows = min(R, rows_all - row0);
+    const int rows = min(R, r.n * G - row0);
     const int tok_first = row0 / G;
-    const int tok_last = (row0 + rows - 1) / G;
+    const int skip = row0 - tok_first * G;
+    const int tok_last = tok_first + tile_token(skip, rows - 1, inv_g);
     const int len = r.ctx + (p.parent ? r.n : tok_last + 1);
     const int steps = (len + St::kStep - 1) / St::kStep;
-    const int s0 = static_cast<int>(part_of(x - it.at, steps, it.cost));
-    const int s1 = static_cast<int>(part_of(till - it.at, steps, it.cost));
+    const int s0 = x == it.at ? 0 : uni(static_cast<int>(part_of(x - it.at, steps, it.cost)));
+    const int s1 =
+        till == end ? steps : uni(static_cast<int>(part_of(till - it.at, steps, it.cost)));
     const bool whole = it.at >= st.lo && end <= st.hi;
     bool good = true;
     if (p.parent) {
       good = tree_masks(p.parent + r.s, r.n, sh.tree);
       if (!good) err |= GDN_DEV_ERR_PARENT;
     }
-    __syncthreads();  // the last item's LDS is free
     if (good) {
-      // Q rows, zero behind the last one
-      constexpr int E = 16 / sizeof(T);
-      const T* q = static_cast<const T*>(p.q) +
-                   (static_cast<size_t>(it.layer) * k.N + r.s) * p.q_ld +
-                   static_cast<size_t>(it.h) * G * D;
-      for (int i = tid; i < R * (D / E); i += W * kWave) {
-        const int row = i / (D / E), ch = i % (D / E);
-        T e[E] = {};
-        if (row < rows) {
-          const int tok = (row0 + row) / G, qh = (row0 + row) % G;
-          *reinterpret_cast<u32x4*>(e) =
-              *reinterpret_cast<const u32x4*>(q + tok * p.q_ld + qh * D + ch * E);
-          if (sgn < 0.f)
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-              if constexpr (sizeof(T) == 2)
-                e[j] ^= 0x8000;
-              else
-                e[j] = -e[j];
-            }
-        }
-        *reinterpret_cast<u32x4*>(&sh.q[row * QLD + ch * E]) = *reinterpret_cast<u32x4*>(e);
-      }
-      // what each of the lane's rows may see: keys below lim, and bits of amask
-      // for the new tokens of a tree
-      int lim[NT];
-      uint64_t amask[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = min(n * 16 + c, rows - 1);
-        const int tok = (row0 + row) / G;
-        lim[n] = p.parent ? r.ctx : r.ctx + tok + 1;
-        amask[n] = p.parent ? sh.tree.mask[tok] : 0;
-      }
-      __syncthreads();
-
-      floatx4 o[NT][MT];
-      float m[NT], l[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m[n] = kNegInf;
-        l[n] = 0.f;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) o[n][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-      }
-      const T* kc = static_cast<const T*>(p.k_cache) +
-                    (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
-      const T* vc = static_cast<const T*>(p.v_cache) +
-                    (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
       const int32_t* table = p.block_table + static_cast<size_t>(it.b) * k.max_blocks;
-      const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
-
       // Page numbers of 32 steps at a time, a lane each: the wave's keys of
       // step first + lane/2, the half lane%2 of them (16 keys lie in one page).
       auto pages_from = [&](int first) {
@@ -297,10 +299,32 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
         }
         return pg;
       };
+      int pgs = pages_from(s0), pgn = -1, batch = s0;
+      // Q rows, zero behind the last one
+      const T* q = static_cast<const T*>(p.q) +
+                   (static_cast<size_t>(it.layer) * k.N + r.s + tok_first) * p.q_ld +
+                   static_cast<size_t>(it.h) * G * D;
+      constexpr int CH = D / VE;  // 16-byte pieces of a row
+      constexpr int QN = (R * CH + W * kWave - 1) / (W * kWave);
+      u32x4 qv[QN];
+#pragma unroll
+      for (int i = 0; i < QN; ++i) {
+        const int at = tid + i * W * kWave, row = at / CH, ch = at % CH;
+        qv[i] = u32x4{0, 0, 0, 0};
+        if (row < rows) {
+          const int tok = tile_token(skip, row, inv_g), qh = skip + row - tok * G;
+          qv[i] = *reinterpret_cast<const u32x4*>(q + tok * p.q_ld + qh * D + ch * VE);
+        }
+      }
+      const T* kc = static_cast<const T*>(p.k_cache) +
+                    (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
+      const T* vc = static_cast<const T*>(p.v_cache) +
+                    (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
+      const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
+
       typename F::K kf[2][KJ];
       typename F::V vf[MT][F::kVLoads];
-      int pgs = pages_from(s0), pgn = -1, batch = s0;
-      int h0 = 0, h1 = 0;  // the current step's page numbers, -1 where nothing is
+      int h0 = 0, h1 = 0;  // the current step's page numbers, below 0 where nothing is
       auto step_pages = [&](int s, int& a, int& e) {
         if (s - batch == 32) {
           pgs = pgn;
@@ -320,7 +344,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int key = F::row_key(t, c);
-          const T* row = (key < 16 ? b0 : b1) + (key & 15) * D + g * (16 / sizeof(T));
+          const T* row = (key < 16 ? b0 : b1) + (key & 15) * D + g * VE;
 #pragma unroll
           for (int j = 0; j < KJ; ++j)
             kf[t][j] = *reinterpret_cast<const typename F::K*>(row + j * F::kPerK);
@@ -343,6 +367,26 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
         load_k(s0, h0, h1);
         load_v(s0, h0, h1);
       }
+      __syncthreads();  // the last item's LDS is free
+      if (tid == 0) sh.any_odd = 0;
+#pragma unroll
+      for (int i = 0; i < QN; ++i) {
+        const int at = tid + i * W * kWave, row = at / CH, ch = at % CH;
+        if (p.scale < 0.f)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qv[i][j] ^= sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+        if (row < R) *reinterpret_cast<u32x4*>(&sh.q[row * QLD + ch * VE]) = qv[i];
+      }
+      floatx4 o[NT][MT];
+      float m[NT], l[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n] = kNegInf;
+        l[n] = 0.f;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) o[n][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+      }
+      __syncthreads();
       for (int s = s0; s < s1; ++s) {
         const int kb = s * St::kStep + wave * 32;
         const int a = h0, e = h1;
@@ -354,7 +398,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 #pragma unroll
           for (int j = 0; j < KJ; ++j) {
             const typename F::K qf = *reinterpret_cast<const typename F::K*>(
-                &sh.q[(n * 16 + c) * QLD + j * F::kPerK + g * (16 / sizeof(T))]);
+                &sh.q[(n * 16 + c) * QLD + j * F::kPerK + g * VE]);
             sc[n][0] = F::score(kf[0][j], qf, sc[n][0]);
             sc[n][1] = F::score(kf[1][j], qf, sc[n][1]);
           }
@@ -364,99 +408,87 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
           load_k(s + 1, h0, h1);
         }
         // any key that some row does not see, or that is not there
-        const bool edge = kb + 32 > r.ctx + (p.parent ? 0 : tok_first + 1) || a < 0 || e < 0;
-        if (edge) {
+        if (kb + 32 > r.ctx + (p.parent ? 0 : tok_first + 1) || a < 0 || e < 0) {
+          uint32_t odd = 0;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int u = 0; u < F::kVLoads; ++u) {
+            // the lane's keys: base .. base + VE - 1, those of tile u (bf16: of both)
+            const int first = F::key_of(u, g, 0), base = kb + first;
+            const uint32_t there = (first < 16 ? a : e) < 0 ? 0u : chain_sees(len, base, VE);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kk = F::key_of(t, g, i), key = kb + kk;
-              const bool there = key < len && (kk < 16 ? a : e) >= 0;
+            for (int n = 0; n < NT; ++n) {
+              const int tok = tok_first + tile_token(skip, min(n * 16 + c, rows - 1), inv_g);
+              const uint32_t sees =
+                  there & (p.parent ? tree_sees(sh.tree.mask[tok], r.ctx, base, VE)
+                                    : chain_sees(r.ctx + tok + 1, base, VE));
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                bool live = there && key < lim[n];
-                if (there && key >= r.ctx && ((amask[n] >> (key - r.ctx)) & 1)) live = true;
-                if (!live) sc[n][t][i] = kNegInf;
+              for (int i = 0; i < VE; ++i) {
+                const int t = VE == 8 ? i / 4 : u;
+                sc[n][t][i % 4] = (sees >> i) & 1 ? sc[n][t][i % 4] : kNegInf;
               }
             }
+            // Values that are not there become 0, and so do infinities and NaN:
+            // 0 * inf would take them to rows that do not see them.
+            const u32x4 keep = F::keep(there);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              const u32x4 w = __builtin_bit_cast(u32x4, vf[t][u]) & keep;
+              vf[t][u] = __builtin_bit_cast(typename F::V, w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) bad |= ((w[j] & F::kExp) + F::kOne) & F::kTop;
+            }
+            if (__any(bad)) {
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                u32x4 w = __builtin_bit_cast(u32x4, vf[t][u]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] &= ~F::spread(((w[j] & F::kExp) + F::kOne) & F::kTop);
+                vf[t][u] = __builtin_bit_cast(typename F::V, w);
+              }
+              odd |= bad;
+            }
+          }
+          if (odd) sh.any_odd = 1;  // rare: rows that do see them get them in the end
+        }
+        // m is the maximum so far, or a number at most kSlack below it in
+        // powers of two: sums stay far from overflow and their precision is the
+        // same, and the rescaling of all outputs is left out while no row's
+        // maximum rises by more.
+        float top[NT];
+        bool rise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float z = fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), fmaxf(sc[n][0][2], sc[n][0][3]));
+          z = fmaxf(z, fmaxf(fmaxf(sc[n][1][0], sc[n][1][1]), fmaxf(sc[n][1][2], sc[n][1][3])));
+          top[n] = row_max(z);
+          rise |= (top[n] - m[n]) * c2 > kSlack;
+        }
+        if (__any(rise)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float M = fmaxf(top[n], m[n]);
+            // a row that has seen no key yet has nothing to rescale
+            const float back = m[n] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m[n] - M) * c2);
+            m[n] = M;
+            l[n] *= back;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][t][i] *= back;
+          }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float top = fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), fmaxf(sc[n][0][2], sc[n][0][3]));
-          top = fmaxf(top, fmaxf(fmaxf(sc[n][1][0], sc[n][1][1]), fmaxf(sc[n][1][2], sc[n][1][3])));
-          top = fmaxf(row_max(top), m[n]);
-          // a row that has seen no key yet: any finite number will do
-          const float at = top == kNegInf ? 0.f : top;
-          const float back = __builtin_amdgcn_exp2f((m[n] - at) * c2);
-          m[n] = top;
-          float add = 0.f;
+          const float at = m[n] == kNegInf ? 0.f : m[n];
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float w = __builtin_amdgcn_exp2f((sc[n][t][i] - at) * c2);
               sc[n][t][i] = w;
-              add += w;
+              l[n] += w;
             }
-          l[n] = l[n] * back + add;
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][t][i] *= back;
-        }
-        if (edge) {
-          // Values that are not there become 0.  An infinity or NaN that only
-          // some rows see would reach the others as 0 * inf: the product is
-          // taken without it, and it is added to the rows that do see it.
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            bool odd = false;
-            constexpr int VE = 16 / sizeof(T);
-#pragma unroll
-            for (int u = 0; u < F::kVLoads; ++u)
-#pragma unroll
-              for (int i = 0; i < VE; ++i) {
-                const int kk = F::key_of(u, g, 0) + i;
-                if (!(kb + kk < len && (kk < 16 ? a : e) >= 0)) vf[t][u][i] = 0;
-                odd |= not_finite(bits(vf[t][u][i]));
-              }
-            if (__any(odd)) {
-#pragma unroll 1
-              for (int kind = 0; kind < 3; ++kind) {
-                const float what = kind == 0   ? __builtin_inff()
-                                   : kind == 1 ? -__builtin_inff()
-                                               : __builtin_nanf("");
-                typename F::V is[F::kVLoads];
-#pragma unroll
-                for (int u = 0; u < F::kVLoads; ++u)
-#pragma unroll
-                  for (int i = 0; i < VE; ++i) {
-                    const uint32_t w = bits(vf[t][u][i]);
-                    const bool hit = kind == 0   ? w == 0x7f800000u
-                                     : kind == 1 ? w == 0xff800000u
-                                                 : (w & 0x7fffffffu) > 0x7f800000u;
-                    is[u][i] = hit ? 1.f : 0.f;
-                  }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  floatx4 seen[2];
-#pragma unroll
-                  for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) seen[t2][i] = sc[n][t2][i] > 0.f ? 1.f : 0.f;
-                  const floatx4 cnt = weigh(is, seen, floatx4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (cnt[i] > 0.f) o[n][t][i] += what;
-                }
-              }
-#pragma unroll
-              for (int u = 0; u < F::kVLoads; ++u)
-#pragma unroll
-                for (int i = 0; i < VE; ++i)
-                  if (not_finite(bits(vf[t][u][i]))) vf[t][u][i] = 0;
-            }
-          }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -465,7 +497,9 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
         if (s + 1 < s1) load_v(s + 1, h0, h1);
       }
 
-      // join the four waves: maxima first, then 16 rows and kC channels at a time
+      // join the four waves: maxima and sums of every row, then the outputs of
+      // kC channels at a time
+      __syncthreads();  // Q's place is free for the outputs
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float sum = row_sum(l[n]);
@@ -476,66 +510,92 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
       }
       __syncthreads();
       const int place = 2 * wg + (it.at < st.lo ? 0 : 1);
-      T* out = static_cast<T*>(p.o) + ((static_cast<size_t>(it.layer) * k.N + r.s) * p.Hq +
-                                       static_cast<size_t>(it.h) * G) * D;
+      const long long out =
+          ((static_cast<long long>(it.layer) * k.N + r.s + tok_first) * p.Hq + it.h * G) * D;
+      float mine[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n * 16 >= rows) break;
         float M = kNegInf;
 #pragma unroll
         for (int w = 0; w < W; ++w) M = fmaxf(M, sh.m[w][n * 16 + c]);
-        const float mine = m[n] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m[n] - M) * c2);
+        mine[n] = m[n] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m[n] - M) * c2);
+      }
+      if (tid < rows) {
+        float M = kNegInf, L = 0.f;
 #pragma unroll
-        for (int ch = 0; ch < D / St::kC; ++ch) {
-          __syncthreads();
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sh.m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (sh.m[w][tid] != kNegInf || sh.l[w][tid] != sh.l[w][tid])
+            L += sh.l[w][tid] * __builtin_amdgcn_exp2f((sh.m[w][tid] - M) * c2);
+        sh.inv[tid] = L == 0.f ? 0.f : 1.f / L;
+        if (!whole) places.ml[static_cast<size_t>(place) * R + tid] = floatx2{M, L};
+      }
+#pragma unroll
+      for (int ch = 0; ch < D / St::kC; ++ch) {
+        if (ch) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int t = 0; t < St::kC / 16; ++t) {
             floatx4 v = o[n][ch * (St::kC / 16) + t];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = mine == 0.f ? 0.f : v[i] * mine;
-            *reinterpret_cast<floatx4*>(&sh.join[wave][c][t * 16 + 4 * g]) = v;
+            for (int i = 0; i < 4; ++i) v[i] = mine[n] == 0.f ? 0.f : v[i] * mine[n];
+            *reinterpret_cast<floatx4*>(&sh.join[wave][n * 16 + c][t * 16 + 4 * g]) = v;
           }
-          __syncthreads();
-          for (int i = tid; i < 16 * St::kC / 4; i += W * kWave) {
-            const int row = i / (St::kC / 4), d = i % (St::kC / 4) * 4;
-            const int rr = n * 16 + row;
-            if (rr >= rows) continue;
-            floatx4 v = *reinterpret_cast<const floatx4*>(&sh.join[0][row][d]);
+        __syncthreads();
+#pragma unroll 2
+        for (int i = tid; i < rows * (St::kC / 4); i += W * kWave) {
+          const int rr = i / (St::kC / 4), d = i % (St::kC / 4) * 4, dd = ch * St::kC + d;
+          floatx4 v = *reinterpret_cast<const floatx4*>(&sh.join[0][rr][d]);
 #pragma unroll
-            for (int w = 1; w < W; ++w) {
-              const floatx4 y = *reinterpret_cast<const floatx4*>(&sh.join[w][row][d]);
+          for (int w = 1; w < W; ++w) {
+            const floatx4 y = *reinterpret_cast<const floatx4*>(&sh.join[w][rr][d]);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] += y[j];
+            for (int j = 0; j < 4; ++j) v[j] += y[j];
+          }
+          const int tok = tile_token(skip, rr, inv_g);
+          if (sh.any_odd) {
+            const int from = max(s0 * St::kStep, r.ctx & ~31), to = min(len, s1 * St::kStep);
+#pragma unroll 1
+            for (int key = from; key < to; ++key) {
+              const bool sees = p.parent ? tree_sees(sh.tree.mask[tok_first + tok], r.ctx, key, 1)
+                                         : key <= r.ctx + tok_first + tok;
+              const int pg = table[key >> k.page_shift];
+              if (!sees || pg < 0 || pg >= k.n_pages) continue;
+              const T* e = vc + static_cast<size_t>(pg) * page_sz +
+                           static_cast<size_t>((key & (ps - 1)) >> 3) * (D * 8) + dd * 8 + (key & 7);
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) {
+                const float y = ld_in(e, j * 8);
+                const float was = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+                const float now = not_finite(y) ? was + y : was;
+                v[0] = j == 0 ? now : v[0];
+                v[1] = j == 1 ? now : v[1];
+                v[2] = j == 2 ? now : v[2];
+                v[3] = j == 3 ? now : v[3];
+              }
             }
-            float Mr = kNegInf, L = 0.f;
+          }
+          if (whole) {
+            const float inv = sh.inv[rr];
+            T* dst = static_cast<T*>(p.o) + out +
+                     (static_cast<long long>(tok) * p.Hq + skip + rr - tok * G) * D + dd;
+            T e4[4];
 #pragma unroll
-            for (int w = 0; w < W; ++w) Mr = fmaxf(Mr, sh.m[w][rr]);
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-              if (sh.m[w][rr] != kNegInf || sh.l[w][rr] != sh.l[w][rr])
-                L += sh.l[w][rr] * __builtin_amdgcn_exp2f((sh.m[w][rr] - Mr) * c2);
-            if (whole) {
-              const int tok = (row0 + rr) / G, qh = (row0 + rr) % G;
-              T* dst = out + (static_cast<size_t>(tok) * p.Hq + qh) * D + ch * St::kC + d;
-              T e4[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) e4[j] = to_out(L == 0.f ? 0.f : v[j] / L, T{});
-              __builtin_memcpy(__builtin_assume_aligned(dst, 4 * sizeof(T)), e4, sizeof(e4));
-            } else {
-              *reinterpret_cast<floatx4*>(
-                  &places.o[(static_cast<size_t>(place) * R + rr) * D + ch * St::kC + d]) = v;
-              if (d == 0 && ch == 0) places.ml[static_cast<size_t>(place) * R + rr] = floatx2{Mr, L};
-            }
+            for (int j = 0; j < 4; ++j) e4[j] = to_out(v[j] * inv, T{});
+            __builtin_memcpy(__builtin_assume_aligned(dst, 4 * sizeof(T)), e4, sizeof(e4));
+          } else {
+            *reinterpret_cast<floatx4*>(
+                &places.o[(static_cast<size_t>(place) * R + rr) * D + dd]) = v;
           }
         }
       }
       if (!whole && it.at >= st.lo) {
         join.last = attn_owner(st.s, end - 1);
         join.rows = rows;
-        join.row0 = row0;
-        join.tok0 = r.s;
-        join.layer = it.layer;
-        join.head = it.h;
+        join.skip = skip;
+        join.out = out;
       }
     }
     x = till;
@@ -547,7 +607,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
           b = 0;
           ++layer;
         }
-        seq_end = seq_at + AttnLine<R>::sequence(kv_span(k, b), G, p.Hkv);
+        r = kv_span(k, b);
+        seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
       }
     }
   }
@@ -556,61 +617,88 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 }
 
 // Adds the fragments of the item that workgroup blockIdx.x began and did not
-// end, in order.  A wave per fragment modulo four, a workgroup per row.
-template <typename T, int D, int R>
+// end, in order of their keys: wave w takes fragments w, w + 4, ..., of RB rows
+// at a time, and the four partial results are added in order.
+template <typename T, int D, int R, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
-  const int w0 = blockIdx.x, row = blockIdx.y;
+  const int w0 = blockIdx.x, row0 = blockIdx.y * RB;
   const AttnJoin j = places.join[w0];
-  if (j.last < 0 || row >= j.rows) return;
+  if (j.last < 0 || row0 >= j.rows) return;
   constexpr int E = D / kWave;
-  __shared__ float sh_m[4], sh_l[4], sh_o[4][D];
+  __shared__ float sh_m[4][RB], sh_l[4][RB], sh_o[4][RB][D];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
-  float m = kNegInf, l = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int w = w0 + wave; w <= j.last; w += 4) {
-    const size_t at = static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * R + row;
-    const floatx2 ml = places.ml[at];
-    float v[E];
+  float m[RB], l[RB], o[RB][E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = places.o[at * D + lane * E + i];
-    if (ml[0] == kNegInf && ml[1] == ml[1]) continue;  // a fragment without keys
-    const float M = fmaxf(m, ml[0]);
-    const float back = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
-    const float add = __builtin_amdgcn_exp2f((ml[0] - M) * c2);
-    m = M;
-    l = l * back + ml[1] * add;
+  for (int y = 0; y < RB; ++y) {
+    m[y] = kNegInf;
+    l[y] = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = (back == 0.f ? 0.f : o[i] * back) + (add == 0.f ? 0.f : v[i] * add);
+    for (int i = 0; i < E; ++i) o[y][i] = 0.f;
   }
-  if (lane == 0) {
-    sh_m[wave] = m;
-    sh_l[wave] = l;
+  constexpr int U = 8 / RB;  // fragments in flight
+  for (int w = w0 + wave; w <= j.last; w += 4 * U) {
+    floatx2 ml[U][RB];
+    float v[U][RB][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int y = 0; y < RB; ++y) {
+        const int f = w + 4 * u;
+        ml[u][y] = floatx2{kNegInf, 0.f};
+        if (f <= j.last && row0 + y < j.rows) {
+          const size_t at = static_cast<size_t>(2 * f + (f == w0 ? 1 : 0)) * R + row0 + y;
+          ml[u][y] = places.ml[at];
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[u][y][i] = places.o[at * D + lane * E + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[u][y][i] = 0.f;
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int y = 0; y < RB; ++y) {
+        if (ml[u][y][0] == kNegInf && ml[u][y][1] == 0.f) continue;  // no keys
+        const float M = fmaxf(m[y], ml[u][y][0]);
+        const float back = m[y] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m[y] - M) * c2);
+        const float add = __builtin_amdgcn_exp2f((ml[u][y][0] - M) * c2);
+        m[y] = M;
+        l[y] = (l[y] == l[y] && back == 0.f ? 0.f : l[y] * back) + ml[u][y][1] * add;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          o[y][i] = (back == 0.f ? 0.f : o[y][i] * back) + (add == 0.f ? 0.f : v[u][y][i] * add);
+      }
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) sh_o[wave][lane * E + i] = o[i];
+  for (int y = 0; y < RB; ++y) {
+    if (lane == 0) {
+      sh_m[wave][y] = m[y];
+      sh_l[wave][y] = l[y];
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) sh_o[wave][y][lane * E + i] = o[y][i];
+  }
   __syncthreads();
-  float M = kNegInf, L = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sh_m[w]);
-  float f[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sh_m[w] == kNegInf && sh_l[w] == sh_l[w] ? 0.f : __builtin_amdgcn_exp2f((sh_m[w] - M) * c2);
-    if (f[w] != 0.f || sh_l[w] != sh_l[w]) L += sh_l[w] * f[w];
-  }
   const int G = p.Hq / p.Hkv;
-  const int tok = (j.row0 + row) / G, qh = (j.row0 + row) % G;
-  T* out = static_cast<T*>(p.o) +
-           ((static_cast<size_t>(j.layer) * p.k.N + j.tok0 + tok) * p.Hq +
-            static_cast<size_t>(j.head) * G + qh) * D;
-  if (static_cast<int>(threadIdx.x) < D) {
-    float v = 0.f;
+  const float inv_g = 1.f / static_cast<float>(G);
+  for (int i = threadIdx.x; i < RB * D; i += 256) {
+    const int y = i / D, d = i % D, row = row0 + y;
+    if (row >= j.rows) continue;
+    float M = kNegInf, L = 0.f, v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      if (f[w] != 0.f) v += sh_o[w][threadIdx.x] * f[w];
-    out[threadIdx.x] = to_out(L == 0.f ? 0.f : v / L, T{});
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, sh_m[w][y]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = sh_m[w][y] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((sh_m[w][y] - M) * c2);
+      if (f != 0.f || sh_l[w][y] != sh_l[w][y]) L += sh_l[w][y] * f;
+      if (f != 0.f) v += sh_o[w][y][d] * f;
+    }
+    const int tok = tile_token(j.skip, row, inv_g);
+    static_cast<T*>(p.o)[j.out + (static_cast<long long>(tok) * p.Hq + j.skip + row - tok * G) * D +
+                         d] = to_out(L == 0.f ? 0.f : v / L, T{});
   }
 }
 
@@ -618,12 +706,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
 constexpr int kStreamWg = 512;
 constexpr long long kGrain = 512;
 
-// Rows of a tile: the fewest 16s that hold a sequence's rows, at most 64 (32
-// with 256 channels, whose sums take the registers).
-int stream_nt(long long rows, int head_dim) {
-  if (rows <= 16) return 1;
-  if (rows <= 32 || head_dim == 256) return 2;
-  return 4;
+// Rows of a tile: the fewest 16s that hold a sequence's rows, as far as their
+// sums, a float per row and channel, stay in registers beside the operands.
+constexpr int stream_most(int head_dim, int size) {
+  const int most = size == 2 ? 512 / head_dim : 256 / head_dim;
+  return most > 4 ? 4 : most < 1 ? 1 : most;
+}
+int stream_nt(long long rows, int head_dim, int size) {
+  const int most = stream_most(head_dim, size);
+  const int want = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  return want < most ? want : most;
 }
 
 template <typename T, int D, int NT>
@@ -632,18 +724,21 @@ hipError_t stream_t(const AttnArgs& a, hipStream_t s) {
   k_attn_stream<T, D, NT><<<kStreamWg, 256, 0, s>>>(a, kStreamWg, kGrain);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_attn_join<T, D, R><<<dim3(kStreamWg, R), 256, 0, s>>>(a, kStreamWg);
+  constexpr int RB = NT;  // 16 workgroups of rows
+  k_attn_join<T, D, R, RB><<<dim3(kStreamWg, R / RB), 256, 0, s>>>(a, kStreamWg);
   return hipGetLastError();
 }
 
 template <typename T, int D>
 hipError_t attn_t(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.k.T) * (a.Hq / a.Hkv);
-  const int nt = stream_nt(rows, D);
-  if (nt == 1) return stream_t<T, D, 1>(a, s);
-  if (nt == 2) return stream_t<T, D, 2>(a, s);
-  if constexpr (D < 256) return stream_t<T, D, 4>(a, s);
-  return hipErrorInvalidValue;
+  constexpr int most = stream_most(D, sizeof(T));
+  const int nt = stream_nt(rows, D, sizeof(T));
+  if constexpr (most >= 4)
+    if (nt == 4) return stream_t<T, D, 4>(a, s);
+  if constexpr (most >= 2)
+    if (nt == 2) return stream_t<T, D, 2>(a, s);
+  return stream_t<T, D, 1>(a, s);
 }
 
 }  // namespace
@@ -663,7 +758,8 @@ hipError_t launch_attn(const AttnArgs& a, int head_dim, int dtype, hipStream_t s
 
 size_t attn_workspace(int L, int B, int T, int N, int Hq, int Hkv, int head_dim, int dtype,
                       long long max_tokens) {
-  const int R = 16 * stream_nt(static_cast<long long>(T) * (Hq / Hkv), head_dim);
+  const int R =
+      16 * stream_nt(static_cast<long long>(T) * (Hq / Hkv), head_dim, dtype == 1 ? 2 : 4);
   return static_cast<size_t>(2 * kStreamWg) * R * (head_dim + 2) * sizeof(float) +
          static_cast<size_t>(kStreamWg) * sizeof(AttnJoin);
 }

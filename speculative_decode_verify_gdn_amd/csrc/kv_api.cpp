@@ -71,6 +71,11 @@ bool ld_ok(const kv_shape* s, int64_t ld, int heads) {
   return ld >= static_cast<int64_t>(heads) * s->head_dim && ld % per == 0 && ld <= (1LL << 20);
 }
 
+// Query rows of a key head are counted in 32 bits.
+bool rows_ok(const kv_shape* s, int32_t n_tokens) {
+  return static_cast<long long>(n_tokens) * (s->n_q_heads / s->n_kv_heads) <= (1LL << 30);
+}
+
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 gdn_status launch_status(hipError_t e) {
@@ -135,7 +140,7 @@ gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int
 
 size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_tokens) {
   if (check_kv(shape) != GDN_OK || T < 1 || n_tokens < 1 || n_tokens > kMaxTokens ||
-      T > kMaxTokens)
+      T > kMaxTokens || !rows_ok(shape, n_tokens))
     return 0;
   return gdn::attn_workspace(shape->n_layers, shape->batch, T, n_tokens, shape->n_q_heads,
                              shape->n_kv_heads, shape->head_dim, shape->dtype,
@@ -155,6 +160,7 @@ gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const
   if (!aligned(q) || !aligned(k_cache) || !aligned(v_cache) || !aligned(o))
     return GDN_ERR_INVALID_ARG;
   if (parent && T > kMaxTree) return GDN_ERR_UNSUPPORTED;
+  if (!rows_ok(shape, n_tokens)) return GDN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace) ||
       workspace_bytes < attn_verify_workspace_bytes(shape, T, n_tokens))
     return GDN_ERR_WORKSPACE;

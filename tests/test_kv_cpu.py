@@ -118,6 +118,8 @@ def test_attention_refusals(lib):
     assert call(a13=ODD) == gb.GDN_ERR_WORKSPACE
     assert call(a14=ws - 1) == gb.GDN_ERR_WORKSPACE
     assert call(a1=65, a2=130, a6=FAKE, a14=1 << 40) == gb.GDN_ERR_UNSUPPORTED  # a tree of 65
+    assert call(a0=shape(Hq=256, Hkv=1), a2=1 << 23, a3=FAKE, a8=1 << 14,
+                a14=1 << 40) == gb.GDN_ERR_UNSUPPORTED  # 2^31 rows of a key head
     assert lib.attn_verify_workspace_bytes(shape(), 0, 8) == 0
     assert lib.attn_verify_workspace_bytes(shape(), 4, 0) == 0
 
