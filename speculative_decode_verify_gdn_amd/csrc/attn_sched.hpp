@@ -135,6 +135,14 @@ __device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long
   a.s.active = a.s.total >= most
                    ? n_wg
                    : static_cast<int>((static_cast<double>(a.s.total) + grain - 1) / grain);
+  // a whole number of workgroups per key head, so that with sequences of one
+  // length, or a single one, no part holds the end of one head and the start
+  // of the next
+  const int heads = p.Hkv * p.L;
+  if (heads <= n_wg) {
+    const int up = (a.s.active + heads - 1) / heads * heads;
+    a.s.active = up <= n_wg ? up : n_wg / heads * heads;
+  }
   a.s.active = uni(a.s.active);
   if (wg >= a.s.active) return a;
   a.lo = uni(part_of(wg, a.s.total, a.s.active));

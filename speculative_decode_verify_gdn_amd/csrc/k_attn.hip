@@ -616,6 +616,386 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
   if (err && p.dev_err) atomicOr(p.dev_err, err);
 }
 
+// ---- many query rows: the waves of a workgroup take different rows
+//
+// R = 128 rows, 32 to a wave, in the lanes (l % 32) of 32x32 result tiles; keys
+// pass through LDS, kKeys at a time, and every wave multiplies with all of
+// them.  v_mfma_f32_32x32x16_bf16: an operand of 1 KB from LDS feeds 32 cycles
+// of a SIMD's products, which is as fast as LDS delivers to four SIMDs, so 32
+// rows to a wave are just enough.
+//
+// Result row m = 8a + 4h + r (h = lane / 32; register 4a + r) stands for key
+// 16 (a / 2) + 8h + 4 (a % 2) + r of its 32: then the eight registers of a = 2s,
+// 2s + 1 are eight consecutive keys, the operand of product step s.
+//
+// LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
+// 32 rows of an operand fall on different banks; values as in the cache, where
+// an operand's 32 channels lie in a row anyway.  Two buffers: while one is
+// multiplied, the next tile is on its way through registers.
+template <int D>
+struct Tile {
+  static constexpr int W = 4;
+  static constexpr int R = 32 * W;
+  static constexpr int kKeys = D <= 128 ? 64 : 32;
+  static constexpr int kPieces = D / 8;                               // 16-byte pieces of a key
+  static constexpr int kLoads = kKeys * kPieces / (W * kWave);        // per thread, K and V each
+  static constexpr int kKeysPerLoad = W * kWave / kPieces;            // of the workgroup
+  struct Lds {
+    u32x4 k[2][kKeys * kPieces];
+    u32x4 v[2][kKeys * kPieces];
+    TreeLds tree;
+  };
+  static __device__ __forceinline__ int swizzle(int key) {
+    return (key & 3) | ((key >> 1) & 4);
+  }
+};
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+template <int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p, int n_wg,
+                                                                    long long grain) {
+  using Tl = Tile<D>;
+  using F = Frag<uint16_t>;
+  constexpr int W = Tl::W, R = Tl::R, KT = Tl::kKeys, P = Tl::kPieces, NL = Tl::kLoads;
+  constexpr int KB = KT / 32;  // score tiles
+  constexpr int QJ = D / 16;   // score products per tile
+  constexpr int DT = D / 32;   // output tiles
+  __shared__ typename Tl::Lds sh;
+  const KvBatch& k = p.k;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = uni(tid / kWave);
+  const int c = lane % 32, h = lane / 32;
+  const int G = p.Hq / p.Hkv;
+  const float inv_g = 1.f / static_cast<float>(G);
+  // neighbours on the line share a head's keys: give them one XCD's L2
+  const int wg = n_wg % kNumXcd == 0
+                     ? static_cast<int>(blockIdx.x) % kNumXcd * (n_wg / kNumXcd) +
+                           static_cast<int>(blockIdx.x) / kNumXcd
+                     : static_cast<int>(blockIdx.x);
+  const Places<R, D> places(p.ws, n_wg);
+  const AttnStart st = attn_start<R>(p, G, wg, n_wg, grain);
+  AttnJoin join;
+  join.last = -1;
+  const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+  const int ps = 1 << k.page_shift;
+  const size_t head_sz = static_cast<size_t>(ps) * D;
+  const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
+  // the key whose row lane c feeds to a score tile
+  const int row_key = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
+  int err = 0;
+
+  long long x = st.lo, seq_at = st.seq_at;
+  int layer = st.layer, b = st.b;
+  KvSpan r = st.span;
+  while (x < st.hi) {
+    const AttnItem it = attn_item<R>(p, G, layer, b, r, seq_at, x);
+    const long long end = it.at + it.cost;
+    const long long till = end < st.hi ? end : st.hi;
+    const int row0 = it.tile * R;
+    const int rows = min(R, r.n * G - row0);
+    const int tok_first = row0 / G;
+    const int skip = row0 - tok_first * G;
+    const int tok_last = tok_first + tile_token(skip, rows - 1, inv_g);
+    const int len = r.ctx + (p.parent ? r.n : tok_last + 1);
+    const int steps = (len + KT - 1) / KT;
+    const int s0 = x == it.at ? 0 : uni(static_cast<int>(part_of(x - it.at, steps, it.cost)));
+    const int s1 =
+        till == end ? steps : uni(static_cast<int>(part_of(till - it.at, steps, it.cost)));
+    const bool whole = it.at >= st.lo && end <= st.hi;
+    bool good = true;
+    if (p.parent) {
+      good = tree_masks(p.parent + r.s, r.n, sh.tree);
+      if (!good) err |= GDN_DEV_ERR_PARENT;
+    }
+    if (good) {
+      const int32_t* table = p.block_table + static_cast<size_t>(it.b) * k.max_blocks;
+      // page numbers of 64 sixteens of keys at a time, a lane each
+      int pgs = -1, pgn = -1, batch = 0;
+      auto pages_from = [&](int first16) {
+        const long long key = (static_cast<long long>(first16) + lane) * 16;
+        int pg = -1;
+        if (key < len && key < static_cast<long long>(s1) * KT) {
+          pg = table[key >> k.page_shift];
+          if (pg < 0 || pg >= k.n_pages) {
+            err |= GDN_DEV_ERR_PAGE;
+            pg = -2;
+          }
+        }
+        return pg;
+      };
+      batch = s0 * (KT / 16);
+      pgs = pages_from(batch);
+      const uint16_t* kc = static_cast<const uint16_t*>(p.k_cache) +
+                           (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
+      const uint16_t* vc = static_cast<const uint16_t*>(p.v_cache) +
+                           (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
+      u32x4 kr[NL], vr[NL];
+      uint32_t gone = 0, gone_next = 0;  // sixteens of the tile that have no page
+      auto fetch = [&](int s) {
+        const int at = s * (KT / 16);
+        if (at - batch == 64) {
+          pgs = pgn;
+          batch = at;
+        }
+        if (at == batch) pgn = pages_from(batch + 64);
+        gone_next = 0;
+#pragma unroll
+        for (int j = 0; j < KT / 16; ++j)
+          if (__builtin_amdgcn_readlane(pgs, at - batch + j) < 0) gone_next |= 1u << j;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          // this wave's keys of load j lie in one sixteen
+          const int i = j * W * kWave + tid;
+          const int kw = uni((j * W * kWave + wave * kWave) / P);  // the wave's first key
+          const int pg = max(__builtin_amdgcn_readlane(pgs, at - batch + kw / 16), 0);
+          const int in_page = (s * KT + (kw & ~15)) & (ps - 1);
+          const int key = i / P, piece = i % P;
+          kr[j] = *reinterpret_cast<const u32x4*>(kc + pg * page_sz +
+                                                  static_cast<size_t>(in_page + (key & 15)) * D +
+                                                  piece * 8);
+          // V pieces: eight keys of a channel
+          const int vg = i / D, ch = i % D;  // group of eight, channel
+          const int vw = uni((j * W * kWave + wave * kWave) / D);
+          const int vpg = max(__builtin_amdgcn_readlane(pgs, at - batch + vw / 2), 0);
+          const int v_in = (s * KT + (vw & ~1) * 8) & (ps - 1);
+          vr[j] = *reinterpret_cast<const u32x4*>(
+              vc + vpg * page_sz + static_cast<size_t>((v_in >> 3) + (vg & 1)) * (D * 8) + ch * 8);
+        }
+      };
+      auto store = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          const int i = j * W * kWave + tid, key = i / P, piece = i % P;
+          sh.k[buf][key * P + (piece ^ Tl::swizzle(key))] = kr[j];
+          sh.v[buf][i] = vr[j];
+        }
+      };
+      if (s0 < s1) fetch(s0);
+
+      // the lane's row
+      const int myrow = min(wave * 32 + c, rows - 1);
+      const int tok = tile_token(skip, myrow, inv_g);
+      const long long out_row =
+          ((static_cast<long long>(it.layer) * k.N + r.s + tok_first + tok) * p.Hq + it.h * G +
+           skip + myrow - tok * G) * D;
+      bf16x8 qf[QJ];
+      {
+        const uint16_t* q =
+            static_cast<const uint16_t*>(p.q) +
+            (static_cast<size_t>(it.layer) * k.N + r.s + tok_first + tok) * p.q_ld +
+            static_cast<size_t>(it.h * G + skip + myrow - tok * G) * D + h * 8;
+#pragma unroll
+        for (int j = 0; j < QJ; ++j) {
+          u32x4 w = *reinterpret_cast<const u32x4*>(q + j * 16);
+          if (p.scale < 0.f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] ^= 0x80008000u;
+          qf[j] = __builtin_bit_cast(bf16x8, w);
+        }
+      }
+      // keys that all of the wave's rows see, and those that any does
+      const int wave_tok0 = tok_first + tile_token(skip, min(wave * 32, rows - 1), inv_g);
+      const int wave_tok1 = tok_first + tile_token(skip, min(wave * 32 + 31, rows - 1), inv_g);
+      const int all_see = r.ctx + (p.parent ? 0 : wave_tok0 + 1);
+      const int any_sees = wave * 32 >= rows ? 0 : p.parent ? len : r.ctx + wave_tok1 + 1;
+      const uint64_t amask = p.parent ? sh.tree.mask[tok_first + tok] : 0;
+      const int lim = r.ctx + tok_first + tok + 1;
+
+      floatx16 o[DT];
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+      float m = kNegInf, l = 0.f;
+      bool odd = false;
+      __syncthreads();  // the last item's LDS is free
+      gone = gone_next;
+      if (s0 < s1) store(0);
+      __syncthreads();
+      for (int s = s0; s < s1; ++s) {
+        const int buf = (s - s0) & 1, kb = s * KT;
+        if (s + 1 < s1) fetch(s + 1);
+        if (kb < any_sees) {
+          floatx16 sc[KB];
+#pragma unroll
+          for (int t = 0; t < KB; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < QJ; ++j) {
+              const int key = t * 32 + row_key;
+              const bf16x8 kf = __builtin_bit_cast(
+                  bf16x8, sh.k[buf][key * P + ((2 * j + h) ^ Tl::swizzle(key))]);
+              sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
+            }
+          }
+          const bool edge = kb + KT > all_see || gone != 0;
+          if (edge) {
+#pragma unroll
+            for (int t = 0; t < KB; ++t)
+#pragma unroll
+              for (int s2 = 0; s2 < 2; ++s2) {
+                const int base = kb + t * 32 + 16 * s2 + 8 * h;  // the lane's eight keys
+                uint32_t sees = chain_sees(len, base, 8);
+                if ((gone >> (t * 2 + s2)) & 1) sees = 0;
+                sees &= p.parent ? tree_sees(amask, r.ctx, base, 8) : chain_sees(lim, base, 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  sc[t][8 * s2 + i] = (sees >> i) & 1 ? sc[t][8 * s2 + i] : kNegInf;
+              }
+          }
+          float top = sc[0][0];
+#pragma unroll
+          for (int t = 0; t < KB; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
+          {
+            const floatx2 two = swap32(top);
+            top = fmaxf(two[0], two[1]);
+          }
+          if (__any((top - m) * c2 > kSlack)) {
+            const float M = fmaxf(top, m);
+            const float back = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
+            m = M;
+            l *= back;
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[t][i] *= back;
+          }
+          const float at = m == kNegInf ? 0.f : m * c2;
+          bf16x8 pf[KB][2];
+#pragma unroll
+          for (int t = 0; t < KB; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float w = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c2, -at));
+              l += w;
+              pf[t][i / 8][i % 8] = static_cast<__bf16>(w);
+            }
+          if (!edge) {
+#pragma unroll
+            for (int t = 0; t < KB; ++t)
+#pragma unroll
+              for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                  const bf16x8 vf = __builtin_bit_cast(
+                      bf16x8, sh.v[buf][(t * 4 + s2 * 2 + h) * D + d * 32 + c]);
+                  o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[t][s2], o[d], 0, 0, 0);
+                }
+          } else {
+            // values that are not there, infinities and NaN are left out here,
+            // as in the stream kernel
+#pragma unroll
+            for (int t = 0; t < KB; ++t)
+#pragma unroll
+              for (int s2 = 0; s2 < 2; ++s2) {
+                const int base = kb + t * 32 + 16 * s2 + 8 * h;
+                const uint32_t there =
+                    (gone >> (t * 2 + s2)) & 1 ? 0u : chain_sees(len, base, 8);
+                const u32x4 keep = F::keep(there);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                  u32x4 w = sh.v[buf][(t * 4 + s2 * 2 + h) * D + d * 32 + c] & keep;
+                  uint32_t bad = 0;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t y = ((w[e] & F::kExp) + F::kOne) & F::kTop;
+                    bad |= y;
+                    w[e] &= ~F::spread(y);
+                  }
+                  odd |= bad != 0;
+                  o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                                 pf[t][s2], o[d], 0, 0, 0);
+                }
+              }
+          }
+        }
+        if (s + 1 < s1) {
+          store(buf ^ 1);
+          gone = gone_next;
+        }
+        __syncthreads();
+      }
+      if (__any(odd)) {  // rare: to the rows that do see them
+        const int from = max(s0 * KT, r.ctx & ~(KT - 1)), to = min(len, s1 * KT);
+#pragma unroll 1
+        for (int key = from; key < to; ++key) {
+          const bool sees = p.parent ? tree_sees(amask, r.ctx, key, 1) != 0 : key < lim;
+          const int pg = table[key >> k.page_shift];
+          if (pg < 0 || pg >= k.n_pages) continue;
+          const uint16_t* e = vc + pg * page_sz +
+                              static_cast<size_t>((key & (ps - 1)) >> 3) * (D * 8) + (key & 7);
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float y = ld_in(e, (t * 32 + 8 * (i / 4) + 4 * h + i % 4) * 8);
+              if (sees && not_finite(y)) o[t][i] += y;
+            }
+        }
+      }
+
+      {
+        const floatx2 two = swap32(l);
+        l = two[0] + two[1];
+      }
+      if (wave * 32 + c < rows) {
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + out_row + 4 * h;
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              uint16_t e4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e4[i] = to_out(o[t][4 * a + i] * inv, uint16_t{});
+              __builtin_memcpy(__builtin_assume_aligned(dst + t * 32 + 8 * a, 8), e4, 8);
+            }
+        } else {
+          const size_t at =
+              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * 32 + c;
+          if (h == 0) places.ml[at] = floatx2{m, l};
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              floatx4 v;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = o[t][4 * a + i];
+              *reinterpret_cast<floatx4*>(&places.o[at * D + t * 32 + 8 * a + 4 * h]) = v;
+            }
+        }
+      }
+      if (!whole && it.at >= st.lo) {
+        join.last = attn_owner(st.s, end - 1);
+        join.rows = rows;
+        join.skip = skip;
+        join.out =
+            ((static_cast<long long>(it.layer) * k.N + r.s + tok_first) * p.Hq + it.h * G) * D;
+      }
+    }
+    x = till;
+    if (x < st.hi) {  // the next item, of this sequence or of the next that has any
+      long long seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+      while (x >= seq_end) {
+        seq_at = seq_end;
+        if (++b == k.B) {
+          b = 0;
+          ++layer;
+        }
+        r = kv_span(k, b);
+        seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+      }
+    }
+  }
+  if (tid == 0) places.join[wg] = join;
+  if (err && p.dev_err) atomicOr(p.dev_err, err);
+}
+
 // Adds the fragments of the item that workgroup blockIdx.x began and did not
 // end, in order of their keys: wave w takes fragments w, w + 4, ..., of RB rows
 // at a time, and the four partial results are added in order.
@@ -637,7 +1017,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
 #pragma unroll
     for (int i = 0; i < E; ++i) o[y][i] = 0.f;
   }
-  constexpr int U = 8 / RB;  // fragments in flight
+  constexpr int U = RB < 8 ? 8 / RB : 1;  // fragments in flight
   for (int w = w0 + wave; w <= j.last; w += 4 * U) {
     floatx2 ml[U][RB];
     float v[U][RB][E];
@@ -702,9 +1082,15 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   }
 }
 
-// Workgroups of the stream kernel: two per CU, each with at least kGrain keys.
-constexpr int kStreamWg = 512;
-constexpr long long kGrain = 512;
+// Two workgroups per CU, each with at least kGrain keys.
+constexpr int kWg = 512;
+constexpr long long kGrain = 256;
+constexpr int kTileR = Tile<128>::R;
+static_assert(Tile<64>::R == kTileR && Tile<256>::R == kTileR, "one workspace rule");
+
+// bf16 batches with more rows to a sequence than the stream kernel holds take
+// the tile kernel.
+bool tiled(long long rows, int dtype) { return dtype == 1 && rows > 64; }
 
 // Rows of a tile: the fewest 16s that hold a sequence's rows, as far as their
 // sums, a float per row and channel, stay in registers beside the operands.
@@ -721,11 +1107,11 @@ int stream_nt(long long rows, int head_dim, int size) {
 template <typename T, int D, int NT>
 hipError_t stream_t(const AttnArgs& a, hipStream_t s) {
   constexpr int R = 16 * NT;
-  k_attn_stream<T, D, NT><<<kStreamWg, 256, 0, s>>>(a, kStreamWg, kGrain);
+  k_attn_stream<T, D, NT><<<kWg, 256, 0, s>>>(a, kWg, kGrain);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int RB = NT;  // 16 workgroups of rows
-  k_attn_join<T, D, R, RB><<<dim3(kStreamWg, R / RB), 256, 0, s>>>(a, kStreamWg);
+  k_attn_join<T, D, R, RB><<<dim3(kWg, R / RB), 256, 0, s>>>(a, kWg);
   return hipGetLastError();
 }
 
@@ -733,6 +1119,14 @@ template <typename T, int D>
 hipError_t attn_t(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.k.T) * (a.Hq / a.Hkv);
   constexpr int most = stream_most(D, sizeof(T));
+  if constexpr (sizeof(T) == 2)
+    if (tiled(rows, 1)) {
+      k_attn_tile<D><<<kWg, 256, 0, s>>>(a, kWg, kGrain);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      k_attn_join<T, D, kTileR, 8><<<dim3(kWg, kTileR / 8), 256, 0, s>>>(a, kWg);
+      return hipGetLastError();
+    }
   const int nt = stream_nt(rows, D, sizeof(T));
   if constexpr (most >= 4)
     if (nt == 4) return stream_t<T, D, 4>(a, s);
@@ -758,10 +1152,10 @@ hipError_t launch_attn(const AttnArgs& a, int head_dim, int dtype, hipStream_t s
 
 size_t attn_workspace(int L, int B, int T, int N, int Hq, int Hkv, int head_dim, int dtype,
                       long long max_tokens) {
-  const int R =
-      16 * stream_nt(static_cast<long long>(T) * (Hq / Hkv), head_dim, dtype == 1 ? 2 : 4);
-  return static_cast<size_t>(2 * kStreamWg) * R * (head_dim + 2) * sizeof(float) +
-         static_cast<size_t>(kStreamWg) * sizeof(AttnJoin);
+  const long long rows = static_cast<long long>(T) * (Hq / Hkv);
+  const int R = tiled(rows, dtype) ? kTileR : 16 * stream_nt(rows, head_dim, dtype == 1 ? 2 : 4);
+  return static_cast<size_t>(2 * kWg) * R * (head_dim + 2) * sizeof(float) +
+         static_cast<size_t>(kWg) * sizeof(AttnJoin);
 }
 
 }  // namespace gdn
