@@ -631,7 +631,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 // LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
 // 32 rows of an operand fall on different banks; values as in the cache, where
 // an operand's 32 channels lie in a row anyway.  Two buffers: while one is
-// multiplied, the next tile is on its way through registers.
+// multiplied, the next tile is loaded into the other, from memory to LDS without
+// a register in between.
 template <int D>
 struct Tile {
   static constexpr int W = 4;
@@ -640,17 +641,22 @@ struct Tile {
   static constexpr int kPieces = D / 8;                               // 16-byte pieces of a key
   static constexpr int kLoads = kKeys * kPieces / (W * kWave);        // per thread, K and V each
   static constexpr int kKeysPerLoad = W * kWave / kPieces;            // of the workgroup
-  struct Lds {
-    u32x4 k[2][kKeys * kPieces];
-    u32x4 v[2][kKeys * kPieces];
-    TreeLds tree;
-  };
   static __device__ __forceinline__ int swizzle(int key) {
     return (key & 3) | ((key >> 1) & 4);
   }
 };
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes per lane, from a uniform address and the lane's own offset in bytes to
+// lane * 16 behind the wave's place.
+__device__ __forceinline__ void to_lds(const uint16_t* from, uint32_t bytes, u32x4* to) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(from) + bytes),
+      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+// Until the wave's loads into LDS have arrived (vmcnt 0).
+__device__ __forceinline__ void lds_loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
 template <int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p, int n_wg,
@@ -661,7 +667,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
   constexpr int KB = KT / 32;  // score tiles
   constexpr int QJ = D / 16;   // score products per tile
   constexpr int DT = D / 32;   // output tiles
-  __shared__ typename Tl::Lds sh;
+  // separate objects, so that the compiler sees that loads into one buffer do
+  // not touch what is read from the other
+  __shared__ u32x4 k_lds0[KT * P], k_lds1[KT * P], v_lds0[KT * P], v_lds1[KT * P];
+  __shared__ TreeLds tree;
   const KvBatch& k = p.k;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = uni(tid / kWave);
@@ -681,8 +690,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
   const int ps = 1 << k.page_shift;
   const size_t head_sz = static_cast<size_t>(ps) * D;
   const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
+  // The lane's offset in a load of keys: its key behind the wave's first, and the
+  // piece that belongs at its place.  A load of the workgroup is 32 or 16 keys, or
+  // 8 (256 channels), when every other one begins in the middle of a sixteen and
+  // permutes differently.
+  constexpr int KP = Tl::kKeysPerLoad >= 16 ? 1 : 2;
+  uint32_t k_off[KP];
+#pragma unroll
+  for (int j = 0; j < KP; ++j) {
+    const int key = (j * W + wave) * kWave / P + lane / P;
+    k_off[j] = (lane / P * D + (lane % P ^ Tl::swizzle(key)) * 8) * 2;
+  }
   // the key whose row lane c feeds to a score tile
   const int row_key = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
+  // pieces 2j + h of that key (the permutation reaches three bits of them)
+  int k_at[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k_at[j] = row_key * P + ((2 * j + h) ^ Tl::swizzle(row_key));
+  const int v_at = h * D + c;
   int err = 0;
 
   long long x = st.lo, seq_at = st.seq_at;
@@ -705,7 +730,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
     const bool whole = it.at >= st.lo && end <= st.hi;
     bool good = true;
     if (p.parent) {
-      good = tree_masks(p.parent + r.s, r.n, sh.tree);
+      good = tree_masks(p.parent + r.s, r.n, tree);
       if (!good) err |= GDN_DEV_ERR_PARENT;
     }
     if (good) {
@@ -730,9 +755,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
                            (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
       const uint16_t* vc = static_cast<const uint16_t*>(p.v_cache) +
                            (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
-      u32x4 kr[NL], vr[NL];
       uint32_t gone = 0, gone_next = 0;  // sixteens of the tile that have no page
-      auto fetch = [&](int s) {
+      // Sends the tile of step s on its way into the buffers: load j of a wave
+      // fills 64 pieces in a row.
+      auto fetch = [&](int s, u32x4* kl, u32x4* vl) {
         const int at = s * (KT / 16);
         if (at - batch == 64) {
           pgs = pgn;
@@ -745,40 +771,25 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
           if (__builtin_amdgcn_readlane(pgs, at - batch + j) < 0) gone_next |= 1u << j;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-          // this wave's keys of load j lie in one sixteen
-          const int i = j * W * kWave + tid;
-          const int kw = uni((j * W * kWave + wave * kWave) / P);  // the wave's first key
+          // everything but the lane's own offset is uniform
+          const int i0 = (j * W + wave) * kWave;
+          // K: the wave's keys of load j lie in one sixteen, on one page
+          const int kw = i0 / P;
           const int pg = max(__builtin_amdgcn_readlane(pgs, at - batch + kw / 16), 0);
-          const int in_page = (s * KT + (kw & ~15)) & (ps - 1);
-          const int key = i / P, piece = i % P;
-          kr[j] = *reinterpret_cast<const u32x4*>(kc + pg * page_sz +
-                                                  static_cast<size_t>(in_page + (key & 15)) * D +
-                                                  piece * 8);
-          // V pieces: eight keys of a channel
-          const int vg = i / D, ch = i % D;  // group of eight, channel
-          const int vw = uni((j * W * kWave + wave * kWave) / D);
+          const int k_in = ((s * KT + (kw & ~15)) & (ps - 1)) + (kw & 15);
+          to_lds(kc + pg * page_sz + k_in * D, k_off[j % KP], kl + i0);
+          // V: eight keys of a channel to a piece
+          const int vw = i0 / D;
           const int vpg = max(__builtin_amdgcn_readlane(pgs, at - batch + vw / 2), 0);
-          const int v_in = (s * KT + (vw & ~1) * 8) & (ps - 1);
-          vr[j] = *reinterpret_cast<const u32x4*>(
-              vc + vpg * page_sz + static_cast<size_t>((v_in >> 3) + (vg & 1)) * (D * 8) + ch * 8);
+          const int v_in = (s * KT + vw * 8) & (ps - 1);
+          to_lds(vc + vpg * page_sz + v_in * D + i0 % D * 8, lane * 16, vl + i0);
         }
       };
-      auto store = [&](int buf) {
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-          const int i = j * W * kWave + tid, key = i / P, piece = i % P;
-          sh.k[buf][key * P + (piece ^ Tl::swizzle(key))] = kr[j];
-          sh.v[buf][i] = vr[j];
-        }
-      };
-      if (s0 < s1) fetch(s0);
-
+      __syncthreads();  // the last item's LDS is free
+      if (s0 < s1) fetch(s0, k_lds0, v_lds0);
       // the lane's row
       const int myrow = min(wave * 32 + c, rows - 1);
       const int tok = tile_token(skip, myrow, inv_g);
-      const long long out_row =
-          ((static_cast<long long>(it.layer) * k.N + r.s + tok_first + tok) * p.Hq + it.h * G +
-           skip + myrow - tok * G) * D;
       bf16x8 qf[QJ];
       {
         const uint16_t* q =
@@ -799,8 +810,6 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
       const int wave_tok1 = tok_first + tile_token(skip, min(wave * 32 + 31, rows - 1), inv_g);
       const int all_see = r.ctx + (p.parent ? 0 : wave_tok0 + 1);
       const int any_sees = wave * 32 >= rows ? 0 : p.parent ? len : r.ctx + wave_tok1 + 1;
-      const uint64_t amask = p.parent ? sh.tree.mask[tok_first + tok] : 0;
-      const int lim = r.ctx + tok_first + tok + 1;
 
       floatx16 o[DT];
 #pragma unroll
@@ -809,13 +818,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
       float m = kNegInf, l = 0.f;
       bool odd = false;
-      __syncthreads();  // the last item's LDS is free
-      gone = gone_next;
-      if (s0 < s1) store(0);
+      lds_loads_done();
       __syncthreads();
-      for (int s = s0; s < s1; ++s) {
-        const int buf = (s - s0) & 1, kb = s * KT;
-        if (s + 1 < s1) fetch(s + 1);
+      auto step = [&](int s, const u32x4* kl, const u32x4* vl) {
+        const int kb = s * KT;
         if (kb < any_sees) {
           floatx16 sc[KB];
 #pragma unroll
@@ -824,9 +830,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
             for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
 #pragma unroll
             for (int j = 0; j < QJ; ++j) {
-              const int key = t * 32 + row_key;
-              const bf16x8 kf = __builtin_bit_cast(
-                  bf16x8, sh.k[buf][key * P + ((2 * j + h) ^ Tl::swizzle(key))]);
+              const bf16x8 kf = __builtin_bit_cast(bf16x8, kl[k_at[j % 4] + t * 32 * P + j / 4 * 8]);
               sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
             }
           }
@@ -839,7 +843,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
                 const int base = kb + t * 32 + 16 * s2 + 8 * h;  // the lane's eight keys
                 uint32_t sees = chain_sees(len, base, 8);
                 if ((gone >> (t * 2 + s2)) & 1) sees = 0;
-                sees &= p.parent ? tree_sees(amask, r.ctx, base, 8) : chain_sees(lim, base, 8);
+                sees &= p.parent ? tree_sees(tree.mask[tok_first + tok], r.ctx, base, 8)
+                                 : chain_sees(r.ctx + tok_first + tok + 1, base, 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                   sc[t][8 * s2 + i] = (sees >> i) & 1 ? sc[t][8 * s2 + i] : kNegInf;
@@ -882,7 +887,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
                   const bf16x8 vf = __builtin_bit_cast(
-                      bf16x8, sh.v[buf][(t * 4 + s2 * 2 + h) * D + d * 32 + c]);
+                      bf16x8, vl[v_at + (t * 4 + s2 * 2) * D + d * 32]);
                   o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[t][s2], o[d], 0, 0, 0);
                 }
           } else {
@@ -898,7 +903,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
                 const u32x4 keep = F::keep(there);
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                  u32x4 w = sh.v[buf][(t * 4 + s2 * 2 + h) * D + d * 32 + c] & keep;
+                  u32x4 w = vl[v_at + (t * 4 + s2 * 2) * D + d * 32] & keep;
                   uint32_t bad = 0;
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
@@ -913,17 +918,26 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
               }
           }
         }
-        if (s + 1 < s1) {
-          store(buf ^ 1);
-          gone = gone_next;
-        }
+      };
+      for (int s = s0; s < s1; s += 2) {
+        gone = gone_next;
+        if (s + 1 < s1) fetch(s + 1, k_lds1, v_lds1);
+        step(s, k_lds0, v_lds0);
+        lds_loads_done();
+        __syncthreads();
+        if (s + 1 == s1) break;
+        gone = gone_next;
+        if (s + 2 < s1) fetch(s + 2, k_lds0, v_lds0);
+        step(s + 1, k_lds1, v_lds1);
+        lds_loads_done();
         __syncthreads();
       }
       if (__any(odd)) {  // rare: to the rows that do see them
         const int from = max(s0 * KT, r.ctx & ~(KT - 1)), to = min(len, s1 * KT);
 #pragma unroll 1
         for (int key = from; key < to; ++key) {
-          const bool sees = p.parent ? tree_sees(amask, r.ctx, key, 1) != 0 : key < lim;
+          const bool sees = p.parent ? tree_sees(tree.mask[tok_first + tok], r.ctx, key, 1) != 0
+                                     : key <= r.ctx + tok_first + tok;
           const int pg = table[key >> k.page_shift];
           if (pg < 0 || pg >= k.n_pages) continue;
           const uint16_t* e = vc + pg * page_sz +
@@ -934,6 +948,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
             for (int i = 0; i < 16; ++i) {
               const float y = ld_in(e, (t * 32 + 8 * (i / 4) + 4 * h + i % 4) * 8);
               if (sees && not_finite(y)) o[t][i] += y;
+              __builtin_amdgcn_sched_barrier(0);  // one at a time: no registers to spare
             }
         }
       }
@@ -945,7 +960,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
       if (wave * 32 + c < rows) {
         if (whole) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* dst = static_cast<uint16_t*>(p.o) + out_row + 4 * h;
+          uint16_t* dst =
+              static_cast<uint16_t*>(p.o) +
+              ((static_cast<long long>(it.layer) * k.N + r.s + tok_first + tok) * p.Hq + it.h * G +
+               skip + myrow - tok * G) * D + 4 * h;
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -997,8 +1015,32 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
 }
 
 // Adds the fragments of the item that workgroup blockIdx.x began and did not
-// end, in order of their keys: wave w takes fragments w, w + 4, ..., of RB rows
-// at a time, and the four partial results are added in order.
+// end, in order of their keys, RB rows at a time.  Four fragments or fewer: each
+// wave takes every fourth row.  More (a long context and few rows): wave w takes
+// fragments w, w + 4, ... of every row, and the four partial results are added
+// in order.
+template <int E>
+struct Partial {
+  float m, l, o[E];
+  __device__ __forceinline__ void clear() {
+    m = kNegInf;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(const Partial& y, float c2) {
+    if (y.m == kNegInf && y.l == 0.f) return;  // no keys
+    const float M = fmaxf(m, y.m);
+    const float a = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
+    const float b = __builtin_amdgcn_exp2f((y.m - M) * c2);
+    // a sum of no weight is left out: it may be an infinity
+    l = (a == 0.f && l == l ? 0.f : l * a) + y.l * b;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = (a == 0.f ? 0.f : o[i] * a) + (b == 0.f ? 0.f : y.o[i] * b);
+    m = M;
+  }
+};
+
 template <typename T, int D, int R, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
@@ -1006,79 +1048,76 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const AttnJoin j = places.join[w0];
   if (j.last < 0 || row0 >= j.rows) return;
   constexpr int E = D / kWave;
-  __shared__ float sh_m[4][RB], sh_l[4][RB], sh_o[4][RB][D];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  __shared__ Partial<E> sh[3][RB][kWave];
+  const int lane = threadIdx.x % kWave, wave = uni(static_cast<int>(threadIdx.x) / kWave);
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
-  float m[RB], l[RB], o[RB][E];
+  const float inv_g = 1.f / static_cast<float>(p.Hq / p.Hkv);
+  const int n = j.last - w0 + 1;
+  auto load = [&](int f, int row) {  // fragment f of a row that is there
+    Partial<E> y;
+    const size_t at = static_cast<size_t>(2 * (w0 + f) + (f == 0 ? 1 : 0)) * R + row;
+    const floatx2 ml = places.ml[at];
+    y.m = ml[0];
+    y.l = ml[1];
 #pragma unroll
-  for (int y = 0; y < RB; ++y) {
-    m[y] = kNegInf;
-    l[y] = 0.f;
+    for (int i = 0; i < E; ++i) y.o[i] = places.o[at * D + lane * E + i];
+    return y;
+  };
+  auto write = [&](const Partial<E>& y, int row) {
+    const int G = p.Hq / p.Hkv, tok = tile_token(j.skip, row, inv_g);
+    T* out = static_cast<T*>(p.o) + j.out +
+             (static_cast<long long>(tok) * p.Hq + j.skip + row - tok * G) * D + lane * E;
+    const float inv = y.l == 0.f ? 0.f : 1.f / y.l;
+    T e[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[y][i] = 0.f;
-  }
-  constexpr int U = RB < 8 ? 8 / RB : 1;  // fragments in flight
-  for (int w = w0 + wave; w <= j.last; w += 4 * U) {
-    floatx2 ml[U][RB];
-    float v[U][RB][E];
+    for (int i = 0; i < E; ++i) e[i] = to_out(y.o[i] * inv, T{});
+    __builtin_memcpy(__builtin_assume_aligned(out, E * sizeof(T)), e, sizeof(e));
+  };
+  if (n <= 4) {
+    constexpr int M = (RB + 3) / 4;
+    Partial<E> y[M][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-      for (int y = 0; y < RB; ++y) {
-        const int f = w + 4 * u;
-        ml[u][y] = floatx2{kNegInf, 0.f};
-        if (f <= j.last && row0 + y < j.rows) {
-          const size_t at = static_cast<size_t>(2 * f + (f == w0 ? 1 : 0)) * R + row0 + y;
-          ml[u][y] = places.ml[at];
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[u][y][i] = places.o[at * D + lane * E + i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[u][y][i] = 0.f;
-        }
+      for (int f = 0; f < 4; ++f) {
+        const int row = row0 + wave + 4 * i;
+        y[i][f].clear();
+        if (f < n && wave + 4 * i < RB && row < j.rows) y[i][f] = load(f, row);
       }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < M; ++i) {
+      const int row = row0 + wave + 4 * i;
+      if (wave + 4 * i >= RB || row >= j.rows) continue;
 #pragma unroll
-      for (int y = 0; y < RB; ++y) {
-        if (ml[u][y][0] == kNegInf && ml[u][y][1] == 0.f) continue;  // no keys
-        const float M = fmaxf(m[y], ml[u][y][0]);
-        const float back = m[y] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m[y] - M) * c2);
-        const float add = __builtin_amdgcn_exp2f((ml[u][y][0] - M) * c2);
-        m[y] = M;
-        l[y] = (l[y] == l[y] && back == 0.f ? 0.f : l[y] * back) + ml[u][y][1] * add;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          o[y][i] = (back == 0.f ? 0.f : o[y][i] * back) + (add == 0.f ? 0.f : v[u][y][i] * add);
-      }
+      for (int f = 1; f < 4; ++f) y[i][0].add(y[i][f], c2);
+      write(y[i][0], row);
+    }
+    return;
   }
+  Partial<E> acc[RB];
 #pragma unroll
-  for (int y = 0; y < RB; ++y) {
-    if (lane == 0) {
-      sh_m[wave][y] = m[y];
-      sh_l[wave][y] = l[y];
+  for (int i = 0; i < RB; ++i) acc[i].clear();
+  for (int f = wave; f < n; f += 4) {
+    Partial<E> y[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      y[i].clear();
+      if (row0 + i < j.rows) y[i] = load(f, row0 + i);
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) sh_o[wave][y][lane * E + i] = o[y][i];
+    for (int i = 0; i < RB; ++i) acc[i].add(y[i], c2);
   }
+  if (wave > 0)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) sh[wave - 1][i][lane] = acc[i];
   __syncthreads();
-  const int G = p.Hq / p.Hkv;
-  const float inv_g = 1.f / static_cast<float>(G);
-  for (int i = threadIdx.x; i < RB * D; i += 256) {
-    const int y = i / D, d = i % D, row = row0 + y;
-    if (row >= j.rows) continue;
-    float M = kNegInf, L = 0.f, v = 0.f;
+  if (wave > 0) return;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, sh_m[w][y]);
+  for (int i = 0; i < RB; ++i) {
+    if (row0 + i >= j.rows) continue;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = sh_m[w][y] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((sh_m[w][y] - M) * c2);
-      if (f != 0.f || sh_l[w][y] != sh_l[w][y]) L += sh_l[w][y] * f;
-      if (f != 0.f) v += sh_o[w][y][d] * f;
-    }
-    const int tok = tile_token(j.skip, row, inv_g);
-    static_cast<T*>(p.o)[j.out + (static_cast<long long>(tok) * p.Hq + j.skip + row - tok * G) * D +
-                         d] = to_out(L == 0.f ? 0.f : v / L, T{});
+    for (int w = 0; w < 3; ++w) acc[i].add(sh[w][i][lane], c2);
+    write(acc[i], row0 + i);
   }
 }
 
