@@ -134,6 +134,12 @@ __device__ __forceinline__ floatx2 swap16(float x) {
                                                   false);
   return floatx2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
+// x, as far as the compiler knows any number: what is computed from it is not
+// moved out of a rare branch into registers that the loop around it needs.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 __device__ __forceinline__ float row_max(float x) {
   const floatx2 a = swap32(x);
   const floatx2 b = swap16(fmaxf(a[0], a[1]));
@@ -650,10 +656,22 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes per lane, from a uniform address and the lane's own offset in bytes to
 // lane * 16 behind the wave's place.
-__device__ __forceinline__ void to_lds(const uint16_t* from, uint32_t bytes, u32x4* to) {
+__device__ __forceinline__ void to_lds(const char* from, uint32_t bytes, u32x4* to) {
   __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(from) + bytes),
+      (const __attribute__((address_space(1))) void*)(from + bytes),
       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+// The order of N products and the LDS reads that feed them, one each: the first
+// `Ahead` reads, then a product and a read in turn.
+template <int N, int Ahead>
+__device__ __forceinline__ void feed() {
+  __builtin_amdgcn_sched_group_barrier(0x100, Ahead, 0);
+#pragma unroll
+  for (int i = 0; i < N - Ahead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, Ahead, 0);
 }
 // Until the wave's loads into LDS have arrived (vmcnt 0).
 __device__ __forceinline__ void lds_loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
@@ -735,8 +753,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
     }
     if (good) {
       const int32_t* table = p.block_table + static_cast<size_t>(it.b) * k.max_blocks;
-      // page numbers of 64 sixteens of keys at a time, a lane each
-      int pgs = -1, pgn = -1, batch = 0;
+      // Pages of 64 sixteens of keys at a time, a lane each: the next ones' numbers
+      // (below 0: none), and the offset in bytes of the current ones' keys in a
+      // cache, which is that of their values too.
+      int pgn, batch = s0 * (KT / 16), off_lo, off_hi;
+      unsigned long long gone_all;
       auto pages_from = [&](int first16) {
         const long long key = (static_cast<long long>(first16) + lane) * 16;
         int pg = -1;
@@ -744,45 +765,48 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
           pg = table[key >> k.page_shift];
           if (pg < 0 || pg >= k.n_pages) {
             err |= GDN_DEV_ERR_PAGE;
-            pg = -2;
+            pg = -1;
           }
         }
         return pg;
       };
-      batch = s0 * (KT / 16);
-      pgs = pages_from(batch);
+      auto enter = [&](int first16, int pg) {
+        batch = first16;
+        gone_all = __ballot(pg < 0);
+        const long long off =
+            (static_cast<long long>(max(pg, 0)) * static_cast<long long>(page_sz) +
+             (((first16 + lane) * 16) & (ps - 1)) * D) * 2;
+        off_lo = static_cast<int>(off);
+        off_hi = static_cast<int>(off >> 32);
+        pgn = pages_from(first16 + 64);
+      };
+      enter(batch, pages_from(batch));
       const uint16_t* kc = static_cast<const uint16_t*>(p.k_cache) +
                            (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
       const uint16_t* vc = static_cast<const uint16_t*>(p.v_cache) +
                            (static_cast<size_t>(it.layer) * k.n_pages * p.Hkv + it.h) * head_sz;
+      const char* kw = reinterpret_cast<const char*>(kc + wave * kWave / P % 16 * D);
+      const char* vw =
+          reinterpret_cast<const char*>(vc + (wave * kWave / D % 2 * D + wave * kWave % D) * 8);
       uint32_t gone = 0, gone_next = 0;  // sixteens of the tile that have no page
       // Sends the tile of step s on its way into the buffers: load j of a wave
-      // fills 64 pieces in a row.
+      // fills 64 pieces in a row, of keys (and of values: eight keys of a channel
+      // to a piece) that lie in one sixteen.
       auto fetch = [&](int s, u32x4* kl, u32x4* vl) {
         const int at = s * (KT / 16);
-        if (at - batch == 64) {
-          pgs = pgn;
-          batch = at;
-        }
-        if (at == batch) pgn = pages_from(batch + 64);
-        gone_next = 0;
-#pragma unroll
-        for (int j = 0; j < KT / 16; ++j)
-          if (__builtin_amdgcn_readlane(pgs, at - batch + j) < 0) gone_next |= 1u << j;
+        if (at - batch == 64) enter(at, pgn);
+        gone_next = static_cast<uint32_t>(gone_all >> (at - batch)) & ((1u << (KT / 16)) - 1u);
+        const int six0 = at - batch + wave * kWave / P / 16;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-          // everything but the lane's own offset is uniform
+          const int six = six0 + j * Tl::kKeysPerLoad / 16;
+          const uint32_t lo = __builtin_amdgcn_readlane(off_lo, six);
+          const uint32_t hi = __builtin_amdgcn_readlane(off_hi, six);
+          const size_t off = (static_cast<size_t>(hi) << 32 | lo) +
+                             j * Tl::kKeysPerLoad % 16 * D * 2;
           const int i0 = (j * W + wave) * kWave;
-          // K: the wave's keys of load j lie in one sixteen, on one page
-          const int kw = i0 / P;
-          const int pg = max(__builtin_amdgcn_readlane(pgs, at - batch + kw / 16), 0);
-          const int k_in = ((s * KT + (kw & ~15)) & (ps - 1)) + (kw & 15);
-          to_lds(kc + pg * page_sz + k_in * D, k_off[j % KP], kl + i0);
-          // V: eight keys of a channel to a piece
-          const int vw = i0 / D;
-          const int vpg = max(__builtin_amdgcn_readlane(pgs, at - batch + vw / 2), 0);
-          const int v_in = (s * KT + vw * 8) & (ps - 1);
-          to_lds(vc + vpg * page_sz + v_in * D + i0 % D * 8, lane * 16, vl + i0);
+          to_lds(kw + off, opaque(k_off[j % KP]), kl + i0);
+          to_lds(vw + off, opaque(lane * 16), vl + i0);
         }
       };
       __syncthreads();  // the last item's LDS is free
@@ -834,13 +858,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
               sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
             }
           }
+          feed<KB * QJ, 4>();
           const bool edge = kb + KT > all_see || gone != 0;
           if (edge) {
 #pragma unroll
             for (int t = 0; t < KB; ++t)
 #pragma unroll
               for (int s2 = 0; s2 < 2; ++s2) {
-                const int base = kb + t * 32 + 16 * s2 + 8 * h;  // the lane's eight keys
+                const int base = kb + t * 32 + 16 * s2 + opaque(8 * h);  // its eight keys
                 uint32_t sees = chain_sees(len, base, 8);
                 if ((gone >> (t * 2 + s2)) & 1) sees = 0;
                 sees &= p.parent ? tree_sees(tree.mask[tok_first + tok], r.ctx, base, 8)
@@ -890,6 +915,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
                       bf16x8, vl[v_at + (t * 4 + s2 * 2) * D + d * 32]);
                   o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[t][s2], o[d], 0, 0, 0);
                 }
+            feed<KB * 2 * DT, 4>();
           } else {
             // values that are not there, infinities and NaN are left out here,
             // as in the stream kernel
@@ -897,7 +923,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
             for (int t = 0; t < KB; ++t)
 #pragma unroll
               for (int s2 = 0; s2 < 2; ++s2) {
-                const int base = kb + t * 32 + 16 * s2 + 8 * h;
+                const int base = kb + t * 32 + 16 * s2 + opaque(8 * h);
                 const uint32_t there =
                     (gone >> (t * 2 + s2)) & 1 ? 0u : chain_sees(len, base, 8);
                 const u32x4 keep = F::keep(there);
@@ -941,12 +967,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
           const int pg = table[key >> k.page_shift];
           if (pg < 0 || pg >= k.n_pages) continue;
           const uint16_t* e = vc + pg * page_sz +
-                              static_cast<size_t>((key & (ps - 1)) >> 3) * (D * 8) + (key & 7);
+                              static_cast<size_t>((key & (ps - 1)) >> 3) * (D * 8) + (key & 7) +
+                              opaque(h * 32);
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float y = ld_in(e, (t * 32 + 8 * (i / 4) + 4 * h + i % 4) * 8);
+              const float y = ld_in(e, (t * 32 + 8 * (i / 4) + i % 4) * 8);
               if (sees && not_finite(y)) o[t][i] += y;
               __builtin_amdgcn_sched_barrier(0);  // one at a time: no registers to spare
             }
@@ -963,7 +990,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
           uint16_t* dst =
               static_cast<uint16_t*>(p.o) +
               ((static_cast<long long>(it.layer) * k.N + r.s + tok_first + tok) * p.Hq + it.h * G +
-               skip + myrow - tok * G) * D + 4 * h;
+               skip + myrow - tok * G) * D + opaque(4 * h);
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -975,7 +1002,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
             }
         } else {
           const size_t at =
-              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * 32 + c;
+              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * 32 + opaque(c);
           if (h == 0) places.ml[at] = floatx2{m, l};
 #pragma unroll
           for (int t = 0; t < DT; ++t)
