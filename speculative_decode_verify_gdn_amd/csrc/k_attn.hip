@@ -17,6 +17,7 @@
 // stores side by side.  No operand is shuffled or passes through LDS but Q.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_sched.hpp"
 #include "gdn_common.hpp"
@@ -624,35 +625,99 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 
 // ---- many query rows: the waves of a workgroup take different rows
 //
-// R = 128 rows, 32 to a wave, in the lanes (l % 32) of 32x32 result tiles; keys
-// pass through LDS, kKeys at a time, and every wave multiplies with all of
-// them.  v_mfma_f32_32x32x16_bf16: an operand of 1 KB from LDS feeds 32 cycles
-// of a SIMD's products, which is as fast as LDS delivers to four SIMDs, so 32
-// rows to a wave are just enough.
+// R = 128 rows; keys pass through LDS, 64 at a time, and every wave multiplies
+// with all of them.  Two forms, by the registers that a row's sums take:
 //
-// Result row m = 8a + 4h + r (h = lane / 32; register 4a + r) stands for key
-// 16 (a / 2) + 8h + 4 (a % 2) + r of its 32: then the eight registers of a = 2s,
-// 2s + 1 are eight consecutive keys, the operand of product step s.
+// Rows32 (64 and 128 channels): 32 rows to a wave, four waves, products of
+// v_mfma_f32_32x32x16_bf16.  Result row m = 8a + 4h + r (h = lane / 32; register
+// 4a + r) stands for key 16 (a / 2) + 8h + 4 (a % 2) + r of its 32: then the eight
+// registers of a = 2s, 2s + 1 are eight consecutive keys, the operand of product
+// step s.
+//
+// Rows16 (256 channels): 16 rows to a wave, eight waves, products of
+// v_mfma_f32_16x16x32_bf16 and keys in the stream kernel's order.  An operand from
+// LDS feeds half as many products, but two waves fit on a SIMD: with 32 rows their
+// sums and queries leave room for one, which waits for every load by itself.
 //
 // LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
-// 32 rows of an operand fall on different banks; values as in the cache, where
-// an operand's 32 channels lie in a row anyway.  Two buffers: while one is
-// multiplied, the next tile is loaded into the other, from memory to LDS without
-// a register in between.
+// rows that are read together fall on different banks; values as in the cache,
+// where an operand's channels lie in a row anyway.  While one tile is multiplied,
+// the next one is loaded into another buffer, from memory to LDS without a
+// register in between.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// One wave's products.  A lane has one row, and of a tile's keys kGroups times
+// eight consecutive ones: from kEvery * i + 8 * part on.
 template <int D>
-struct Tile {
-  static constexpr int W = 4;
-  static constexpr int R = 32 * W;
-  static constexpr int kKeys = D <= 128 ? 64 : 32;
-  static constexpr int kPieces = D / 8;                               // 16-byte pieces of a key
-  static constexpr int kLoads = kKeys * kPieces / (W * kWave);        // per thread, K and V each
-  static constexpr int kKeysPerLoad = W * kWave / kPieces;            // of the workgroup
+struct Rows32 {
+  static constexpr int kRows = 32, kWaves = 4, kMinWaves = 2;
+  static constexpr int kGroups = 4, kEvery = 16;
+  static constexpr int QJ = D / 16, DT = D / 32;  // score products, output tiles
+  static constexpr int kQ = 16;                   // channels of a score product
+  typedef floatx16 Acc;
+  static constexpr int kAcc = 16;
+  static __device__ __forceinline__ int row_key(int c) {
+    return 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
+  }
+  // 16 rows in a row are served together: keys that differ in four bits
   static __device__ __forceinline__ int swizzle(int key) {
-    return (key & 3) | ((key >> 1) & 4);
+    return D == 64 ? (key >> 1) & 7 : key & 15;
+  }
+  static constexpr int kScoreTiles = 2;  // of 64 keys
+  static __device__ __forceinline__ Acc mul(bf16x8 a, bf16x8 b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  // the keys of score tile t begin here
+  static __device__ __forceinline__ constexpr int tile_key(int t) { return 32 * t; }
+  // score tile and register of key e of group i
+  static __device__ __forceinline__ constexpr int tile_of(int i, int) { return i / 2; }
+  static __device__ __forceinline__ constexpr int reg_of(int i, int e) { return 8 * (i % 2) + e; }
+  // channel of register r of an output tile, behind 4 * part
+  static __device__ __forceinline__ constexpr int channel(int r) { return 8 * (r / 4) + r % 4; }
+  static __device__ __forceinline__ float top(float x) {
+    const floatx2 a = swap32(x);
+    return fmaxf(a[0], a[1]);
+  }
+  static __device__ __forceinline__ float sum(float x) {
+    const floatx2 a = swap32(x);
+    return a[0] + a[1];
   }
 };
 
-typedef float floatx16 __attribute__((ext_vector_type(16)));
+template <int D>
+struct Rows16 {
+  static constexpr int kRows = 16, kWaves = 8, kMinWaves = 2;
+  static constexpr int kGroups = 2, kEvery = 32;
+  static constexpr int QJ = D / 32, DT = D / 16;
+  static constexpr int kQ = 32;
+  typedef floatx4 Acc;
+  static constexpr int kAcc = 4;
+  static __device__ __forceinline__ int row_key(int c) { return 8 * (c >> 2) + (c & 3); }
+  static __device__ __forceinline__ int swizzle(int key) {
+    return (key & 3) | (key >> 1 & 12);  // a score tile's keys differ in these
+  }
+  static constexpr int kScoreTiles = 4;
+  static __device__ __forceinline__ Acc mul(bf16x8 a, bf16x8 b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ constexpr int tile_key(int t) { return t / 2 * 32 + t % 2 * 4; }
+  static __device__ __forceinline__ constexpr int tile_of(int i, int e) { return 2 * i + e / 4; }
+  static __device__ __forceinline__ constexpr int reg_of(int, int e) { return e % 4; }
+  static __device__ __forceinline__ constexpr int channel(int r) { return r; }
+  static __device__ __forceinline__ float top(float x) { return row_max(x); }
+  static __device__ __forceinline__ float sum(float x) { return row_sum(x); }
+};
+
+template <int D>
+struct Tile {
+  typedef typename std::conditional<D == 256, Rows16<D>, Rows32<D>>::type Mma;
+  static constexpr int W = Mma::kWaves;
+  static constexpr int R = Mma::kRows * W;
+  static constexpr int kKeys = 64;
+  static constexpr int kPieces = D / 8;                         // 16-byte pieces of a key
+  static constexpr int kLoads = kKeys * kPieces / (W * kWave);  // of a wave, K and V each
+  static constexpr int kKeysPerLoad = W * kWave / kPieces;      // of the workgroup
+};
 
 // 16 bytes per lane, from a uniform address and the lane's own offset in bytes to
 // lane * 16 behind the wave's place.
@@ -661,38 +726,61 @@ __device__ __forceinline__ void to_lds(const char* from, uint32_t bytes, u32x4* 
       (const __attribute__((address_space(1))) void*)(from + bytes),
       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
-// The order of N products and the LDS reads that feed them, one each: the first
-// `Ahead` reads, then a product and a read in turn.
-template <int N, int Ahead>
-__device__ __forceinline__ void feed() {
-  __builtin_amdgcn_sched_group_barrier(0x100, Ahead, 0);
-#pragma unroll
-  for (int i = 0; i < N - Ahead; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, Ahead, 0);
+// A barrier for what the waves read from LDS: their reads have returned, and
+// loads into LDS that are still under way stay so (__syncthreads would wait for
+// those too).
+__device__ __forceinline__ void lds_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
-// Until the wave's loads into LDS have arrived (vmcnt 0).
-__device__ __forceinline__ void lds_loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// N products whose operands read(n) fetches from LDS kAhead products ahead, in this
+// order whatever the compiler would prefer: no product waits for its operand, and
+// no more registers hold operands than that.
+constexpr int kAhead = 4;
+template <int N, typename Read, typename Mul>
+__device__ __forceinline__ void products(Read read, Mul mul) {
+  static_assert(N % kAhead == 0, "the ring comes round");
+  bf16x8 f[kAhead];
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) f[n] = read(n);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    mul(n, f[n % kAhead]);
+    if (n + kAhead < N) f[n % kAhead] = read(n + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+// Until all but the last N of the wave's loads into LDS have arrived (vmcnt N).
+template <int N>
+__device__ __forceinline__ void lds_loads_done() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
+}
 
 template <int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p, int n_wg,
-                                                                    long long grain) {
+__global__ __launch_bounds__(Tile<D>::W * kWave, Tile<D>::Mma::kMinWaves) void k_attn_tile(
+    AttnArgs p, int n_wg, long long grain) {
   using Tl = Tile<D>;
+  using Mm = typename Tl::Mma;
+  typedef typename Mm::Acc Acc;
   using F = Frag<uint16_t>;
   constexpr int W = Tl::W, R = Tl::R, KT = Tl::kKeys, P = Tl::kPieces, NL = Tl::kLoads;
-  constexpr int KB = KT / 32;  // score tiles
-  constexpr int QJ = D / 16;   // score products per tile
-  constexpr int DT = D / 32;   // output tiles
+  constexpr int KB = Mm::kScoreTiles, QJ = Mm::QJ, DT = Mm::DT, NG = Mm::kGroups;
+  constexpr int MR = Mm::kRows, PT = kWave / MR;  // rows of a wave, lanes of a row
   // separate objects, so that the compiler sees that loads into one buffer do
   // not touch what is read from the other
-  __shared__ u32x4 k_lds0[KT * P], k_lds1[KT * P], v_lds0[KT * P], v_lds1[KT * P];
+  constexpr int NS = 2, kBuf = 2 * KT * P;
+  __shared__ u32x4 lds0[kBuf], lds1[kBuf];  // keys, then values
+  auto buf = [&](int i) { return i == 0 ? lds0 : lds1; };
   __shared__ TreeLds tree;
   const KvBatch& k = p.k;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = uni(tid / kWave);
-  const int c = lane % 32, h = lane / 32;
+  const int c = lane % MR, h = lane / MR;  // row, part
   const int G = p.Hq / p.Hkv;
   const float inv_g = 1.f / static_cast<float>(G);
   // neighbours on the line share a head's keys: give them one XCD's L2
@@ -709,22 +797,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
   const size_t head_sz = static_cast<size_t>(ps) * D;
   const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
   // The lane's offset in a load of keys: its key behind the wave's first, and the
-  // piece that belongs at its place.  A load of the workgroup is 32 or 16 keys, or
-  // 8 (256 channels), when every other one begins in the middle of a sixteen and
-  // permutes differently.
-  constexpr int KP = Tl::kKeysPerLoad >= 16 ? 1 : 2;
+  // piece that belongs at its place.  With 256 channels a load of the workgroup is
+  // 16 keys, and every other one permutes differently.
+  constexpr int KP = D == 256 ? 2 : 1;
   uint32_t k_off[KP];
 #pragma unroll
   for (int j = 0; j < KP; ++j) {
     const int key = (j * W + wave) * kWave / P + lane / P;
-    k_off[j] = (lane / P * D + (lane % P ^ Tl::swizzle(key)) * 8) * 2;
+    k_off[j] = (lane / P * D + (lane % P ^ Mm::swizzle(key)) * 8) * 2;
   }
-  // the key whose row lane c feeds to a score tile
-  const int row_key = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
-  // pieces 2j + h of that key (the permutation reaches three bits of them)
-  int k_at[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) k_at[j] = row_key * P + ((2 * j + h) ^ Tl::swizzle(row_key));
+  // the key whose row lane c feeds to a score tile, and its piece h; piece PT j + h
+  // is at k_at ^ PT j (tile keys leave the permutation as it is)
+  const int row_key = Mm::row_key(c);
+  const int k_at = row_key * P + (h ^ Mm::swizzle(row_key));
   const int v_at = h * D + c;
   int err = 0;
 
@@ -758,23 +843,23 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
       // cache, which is that of their values too.
       int pgn, batch = s0 * (KT / 16), off_lo, off_hi;
       unsigned long long gone_all;
-      auto pages_from = [&](int first16) {
+      auto has_key = [&](int first16) {
         const long long key = (static_cast<long long>(first16) + lane) * 16;
-        int pg = -1;
-        if (key < len && key < static_cast<long long>(s1) * KT) {
-          pg = table[key >> k.page_shift];
-          if (pg < 0 || pg >= k.n_pages) {
-            err |= GDN_DEV_ERR_PAGE;
-            pg = -1;
-          }
-        }
-        return pg;
+        return key < len && key < static_cast<long long>(s1) * KT;
+      };
+      // As they stand in the table, or any entry where there is no key: nothing
+      // here depends on the number, so that nothing waits for it before its turn.
+      auto pages_from = [&](int first16) {
+        return table[has_key(first16) ? ((first16 + lane) * 16) >> k.page_shift : 0];
       };
       auto enter = [&](int first16, int pg) {
         batch = first16;
-        gone_all = __ballot(pg < 0);
+        const bool bad = pg < 0 || pg >= k.n_pages;
+        const bool none = bad || !has_key(first16);
+        if (none && has_key(first16)) err |= GDN_DEV_ERR_PAGE;
+        gone_all = __ballot(none);
         const long long off =
-            (static_cast<long long>(max(pg, 0)) * static_cast<long long>(page_sz) +
+            (static_cast<long long>(none ? 0 : pg) * static_cast<long long>(page_sz) +
              (((first16 + lane) * 16) & (ps - 1)) * D) * 2;
         off_lo = static_cast<int>(off);
         off_hi = static_cast<int>(off >> 32);
@@ -788,14 +873,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
       const char* kw = reinterpret_cast<const char*>(kc + wave * kWave / P % 16 * D);
       const char* vw =
           reinterpret_cast<const char*>(vc + (wave * kWave / D % 2 * D + wave * kWave % D) * 8);
-      uint32_t gone = 0, gone_next = 0;  // sixteens of the tile that have no page
+      uint32_t gones = 0;
+      // Sixteens without a page, of all tiles in flight; a tile's are looked at
+      // when it is multiplied (only then does a page number that is not one count).
       // Sends the tile of step s on its way into the buffers: load j of a wave
       // fills 64 pieces in a row, of keys (and of values: eight keys of a channel
       // to a piece) that lie in one sixteen.
-      auto fetch = [&](int s, u32x4* kl, u32x4* vl) {
+      auto fetch = [&](int s, u32x4* kl) {
+        u32x4* const vl = kl + KT * P;
         const int at = s * (KT / 16);
         if (at - batch == 64) enter(at, pgn);
-        gone_next = static_cast<uint32_t>(gone_all >> (at - batch)) & ((1u << (KT / 16)) - 1u);
+        gones = gones << (KT / 16) |
+                (static_cast<uint32_t>(gone_all >> (at - batch)) & ((1u << (KT / 16)) - 1u));
         const int six0 = at - batch + wave * kWave / P / 16;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -810,9 +899,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
         }
       };
       __syncthreads();  // the last item's LDS is free
-      if (s0 < s1) fetch(s0, k_lds0, v_lds0);
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i)
+        if (s0 + i < s1) fetch(s0 + i, buf(i));
       // the lane's row
-      const int myrow = min(wave * 32 + c, rows - 1);
+      const int myrow = min(wave * MR + c, rows - 1);
       const int tok = tile_token(skip, myrow, inv_g);
       bf16x8 qf[QJ];
       {
@@ -822,141 +913,159 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
             static_cast<size_t>(it.h * G + skip + myrow - tok * G) * D + h * 8;
 #pragma unroll
         for (int j = 0; j < QJ; ++j) {
-          u32x4 w = *reinterpret_cast<const u32x4*>(q + j * 16);
+          u32x4 w = *reinterpret_cast<const u32x4*>(q + j * Mm::kQ);
           if (p.scale < 0.f)
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] ^= 0x80008000u;
           qf[j] = __builtin_bit_cast(bf16x8, w);
         }
       }
-      // keys that all of the wave's rows see, and those that any does
-      const int wave_tok0 = tok_first + tile_token(skip, min(wave * 32, rows - 1), inv_g);
-      const int wave_tok1 = tok_first + tile_token(skip, min(wave * 32 + 31, rows - 1), inv_g);
-      const int all_see = r.ctx + (p.parent ? 0 : wave_tok0 + 1);
-      const int any_sees = wave * 32 >= rows ? 0 : p.parent ? len : r.ctx + wave_tok1 + 1;
+      // keys that all rows see, and those that any of the wave's does
+      const int wave_tok1 = tok_first + tile_token(skip, min(wave * MR + MR - 1, rows - 1), inv_g);
+      const int all_see = r.ctx + (p.parent ? 0 : tok_first + 1);
+      const int any_sees = wave * MR >= rows ? 0 : p.parent ? len : r.ctx + wave_tok1 + 1;
 
-      floatx16 o[DT];
+      Acc o[DT];
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+      for (int t = 0; t < DT; ++t) o[t] = Acc{};
       float m = kNegInf, l = 0.f;
       bool odd = false;
-      lds_loads_done();
-      __syncthreads();
-      auto step = [&](int s, const u32x4* kl, const u32x4* vl) {
-        const int kb = s * KT;
-        if (kb < any_sees) {
-          floatx16 sc[KB];
+      auto scores = [&](Acc* sc, const u32x4* kl) {
+        const int ka = opaque(k_at);  // the operands' places are worked out anew: few registers
+        products<KB * QJ>(
+            [&](int n) {
+              return __builtin_bit_cast(
+                  bf16x8, kl[(ka ^ PT * (n % QJ)) + Mm::tile_key(n / QJ) * P]);
+            },
+            [&](int n, bf16x8 kf) {
+              Acc& z = sc[n / QJ];
+              if (n % QJ == 0) z = Acc{};
+              z = Mm::mul(kf, qf[n % QJ], z);
+            });
+      };
+      // Raises the maximum where it has to, then turns scores into probabilities.
+      auto weights = [&](const Acc* sc, bf16x8* pf) {
+        float top = sc[0][0];
 #pragma unroll
-          for (int t = 0; t < KB; ++t) {
+        for (int t = 0; t < KB; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+          for (int i = 0; i < Mm::kAcc; ++i) top = fmaxf(top, sc[t][i]);
+        top = Mm::top(top);
+        if (__any((top - m) * c2 > kSlack)) {
+          const float M = fmaxf(top, m);
+          const float back = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
+          m = M;
+          l *= back;
 #pragma unroll
-            for (int j = 0; j < QJ; ++j) {
-              const bf16x8 kf = __builtin_bit_cast(bf16x8, kl[k_at[j % 4] + t * 32 * P + j / 4 * 8]);
-              sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
-            }
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < Mm::kAcc; ++i) o[t][i] *= back;
+        }
+        const float at = m == kNegInf ? 0.f : m * c2;
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w =
+                __builtin_amdgcn_exp2f(fmaf(sc[Mm::tile_of(i, e)][Mm::reg_of(i, e)], c2, -at));
+            l += w;
+            pf[i][e] = static_cast<__bf16>(w);
           }
-          feed<KB * QJ, 4>();
-          const bool edge = kb + KT > all_see || gone != 0;
-          if (edge) {
+      };
+      const auto value_at = [&](int n) {  // operand n of the products with the values
+        return v_at + n / DT * (Mm::kEvery / 8) * D + n % DT * MR;
+      };
+      // A tile that every row sees all of.
+      auto plain = [&](const u32x4* kl) {
+        const u32x4* const vl = kl + KT * P;
+        if (any_sees == 0) return;  // a wave without rows
+        Acc sc[KB];
+        bf16x8 pf[NG];
+        scores(sc, kl);
+        weights(sc, pf);
+        products<NG * DT>(
+            [&](int n) { return __builtin_bit_cast(bf16x8, vl[value_at(n)]); },
+            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
+      };
+      // A tile with keys that some row does not see or that are not there.
+      // Values that are not there, infinities and NaN are left out, as in the
+      // stream kernel.
+      auto edge = [&](int kb, uint32_t gone, const u32x4* kl) {
+        const u32x4* const vl = kl + KT * P;
+        if (kb >= any_sees) return;
+        Acc sc[KB];
+        bf16x8 pf[NG];
+        scores(sc, kl);
+        // the first of the lane's eight keys of group i, and those of them that are there
+        auto base_of = [&](int i) { return kb + Mm::kEvery * i + opaque(8 * h); };
+        auto there_of = [&](int i, int base) {
+          return (gone >> ((base - kb) / 16)) & 1 ? 0u : chain_sees(len, base, 8);
+        };
 #pragma unroll
-            for (int t = 0; t < KB; ++t)
+        for (int i = 0; i < NG; ++i) {
+          const int base = base_of(i);
+          uint32_t sees = there_of(i, base);
+          sees &= p.parent ? tree_sees(tree.mask[tok_first + tok], r.ctx, base, 8)
+                           : chain_sees(r.ctx + tok_first + tok + 1, base, 8);
 #pragma unroll
-              for (int s2 = 0; s2 < 2; ++s2) {
-                const int base = kb + t * 32 + 16 * s2 + opaque(8 * h);  // its eight keys
-                uint32_t sees = chain_sees(len, base, 8);
-                if ((gone >> (t * 2 + s2)) & 1) sees = 0;
-                sees &= p.parent ? tree_sees(tree.mask[tok_first + tok], r.ctx, base, 8)
-                                 : chain_sees(r.ctx + tok_first + tok + 1, base, 8);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  sc[t][8 * s2 + i] = (sees >> i) & 1 ? sc[t][8 * s2 + i] : kNegInf;
-              }
-          }
-          float top = sc[0][0];
-#pragma unroll
-          for (int t = 0; t < KB; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
-          {
-            const floatx2 two = swap32(top);
-            top = fmaxf(two[0], two[1]);
-          }
-          if (__any((top - m) * c2 > kSlack)) {
-            const float M = fmaxf(top, m);
-            const float back = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
-            m = M;
-            l *= back;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[t][i] *= back;
-          }
-          const float at = m == kNegInf ? 0.f : m * c2;
-          bf16x8 pf[KB][2];
-#pragma unroll
-          for (int t = 0; t < KB; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float w = __builtin_amdgcn_exp2f(fmaf(sc[t][i], c2, -at));
-              l += w;
-              pf[t][i / 8][i % 8] = static_cast<__bf16>(w);
-            }
-          if (!edge) {
-#pragma unroll
-            for (int t = 0; t < KB; ++t)
-#pragma unroll
-              for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                  const bf16x8 vf = __builtin_bit_cast(
-                      bf16x8, vl[v_at + (t * 4 + s2 * 2) * D + d * 32]);
-                  o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[t][s2], o[d], 0, 0, 0);
-                }
-            feed<KB * 2 * DT, 4>();
-          } else {
-            // values that are not there, infinities and NaN are left out here,
-            // as in the stream kernel
-#pragma unroll
-            for (int t = 0; t < KB; ++t)
-#pragma unroll
-              for (int s2 = 0; s2 < 2; ++s2) {
-                const int base = kb + t * 32 + 16 * s2 + opaque(8 * h);
-                const uint32_t there =
-                    (gone >> (t * 2 + s2)) & 1 ? 0u : chain_sees(len, base, 8);
-                const u32x4 keep = F::keep(there);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                  u32x4 w = vl[v_at + (t * 4 + s2 * 2) * D + d * 32] & keep;
-                  uint32_t bad = 0;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const uint32_t y = ((w[e] & F::kExp) + F::kOne) & F::kTop;
-                    bad |= y;
-                    w[e] &= ~F::spread(y);
-                  }
-                  odd |= bad != 0;
-                  o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
-                                                                 pf[t][s2], o[d], 0, 0, 0);
-                }
-              }
+          for (int e = 0; e < 8; ++e) {
+            float z = sc[Mm::tile_of(i, e)][Mm::reg_of(i, e)];
+            sc[Mm::tile_of(i, e)][Mm::reg_of(i, e)] = (sees >> e) & 1 ? z : kNegInf;
           }
         }
+        weights(sc, pf);
+        u32x4 keep[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) keep[i] = F::keep(there_of(i, base_of(i)));
+        uint32_t bad = 0;
+        products<NG * DT>(
+            [&](int n) {
+              u32x4 w = vl[value_at(n)] & keep[n / DT];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t y = ((w[e] & F::kExp) + F::kOne) & F::kTop;
+                bad |= y;
+                w[e] &= ~F::spread(y);
+              }
+              return __builtin_bit_cast(bf16x8, w);
+            },
+            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
+        odd |= bad != 0;
       };
-      for (int s = s0; s < s1; s += 2) {
-        gone = gone_next;
-        if (s + 1 < s1) fetch(s + 1, k_lds1, v_lds1);
-        step(s, k_lds0, v_lds0);
-        lds_loads_done();
-        __syncthreads();
-        if (s + 1 == s1) break;
-        gone = gone_next;
-        if (s + 2 < s1) fetch(s + 2, k_lds0, v_lds0);
-        step(s + 1, k_lds1, v_lds1);
-        lds_loads_done();
-        __syncthreads();
+
+      // What is in flight when tile s is needed: of NS - 1 tiles, all but the
+      // oldest may stay so, unless no more are being sent.
+      lds_loads_done<0>();
+      lds_barrier();
+      int s = s0, at = 0;  // at = (s - s0) % NS
+      auto is_gone = [&](int step) {  // of tile `step`, the oldest in flight
+        const int newer = min(step + NS - 2, s1 - 1) - step;
+        return gones >> (newer * (KT / 16)) & ((1u << (KT / 16)) - 1u);
+      };
+      while (s < s1 && (s + 1) * KT <= all_see && is_gone(s) == 0) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const bool more = s + NS - 1 < s1;
+          if (more) fetch(s + NS - 1, buf((i + NS - 1) % NS));
+          plain(buf(i));
+          if (more)
+            lds_loads_done<(NS - 2) * 2 * NL>();
+          else
+            lds_loads_done<0>();
+          lds_barrier();
+          ++s;
+          at = (i + 1) % NS;
+          if (!(s < s1 && (s + 1) * KT <= all_see && is_gone(s) == 0)) break;
+        }
+      }
+      for (; s < s1; ++s) {
+        const uint32_t gone = is_gone(s);
+        const int to = (at + NS - 1) % NS;
+        if (s + NS - 1 < s1) fetch(s + NS - 1, buf(to));
+        edge(s * KT, gone, buf(at));
+        lds_loads_done<0>();
+        lds_barrier();
+        at = (at + 1) % NS;
       }
       if (__any(odd)) {  // rare: to the rows that do see them
         const int from = max(s0 * KT, r.ctx & ~(KT - 1)), to = min(len, s1 * KT);
@@ -972,19 +1081,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float y = ld_in(e, (t * 32 + 8 * (i / 4) + i % 4) * 8);
+            for (int i = 0; i < Mm::kAcc; ++i) {
+              const float y = ld_in(e, (t * MR + Mm::channel(i)) * 8);
               if (sees && not_finite(y)) o[t][i] += y;
               __builtin_amdgcn_sched_barrier(0);  // one at a time: no registers to spare
             }
         }
       }
 
-      {
-        const floatx2 two = swap32(l);
-        l = two[0] + two[1];
-      }
-      if (wave * 32 + c < rows) {
+      l = Mm::sum(l);
+      if (wave * MR + c < rows) {
         if (whole) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           uint16_t* dst =
@@ -994,24 +1100,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p,
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+            for (int a = 0; a < Mm::kAcc / 4; ++a) {
               uint16_t e4[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) e4[i] = to_out(o[t][4 * a + i] * inv, uint16_t{});
-              __builtin_memcpy(__builtin_assume_aligned(dst + t * 32 + 8 * a, 8), e4, 8);
+              __builtin_memcpy(__builtin_assume_aligned(dst + t * MR + 8 * a, 8), e4, 8);
             }
         } else {
           const size_t at =
-              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * 32 + opaque(c);
+              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * MR + opaque(c);
           if (h == 0) places.ml[at] = floatx2{m, l};
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+            for (int a = 0; a < Mm::kAcc / 4; ++a) {
               floatx4 v;
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[i] = o[t][4 * a + i];
-              *reinterpret_cast<floatx4*>(&places.o[at * D + t * 32 + 8 * a + 4 * h]) = v;
+              *reinterpret_cast<floatx4*>(&places.o[at * D + t * MR + 8 * a + 4 * h]) = v;
             }
         }
       }
@@ -1151,6 +1257,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
 // Two workgroups per CU, each with at least kGrain keys.
 constexpr int kWg = 512;
 constexpr long long kGrain = 256;
+
 constexpr int kTileR = Tile<128>::R;
 static_assert(Tile<64>::R == kTileR && Tile<256>::R == kTileR, "one workspace rule");
 
@@ -1187,10 +1294,11 @@ hipError_t attn_t(const AttnArgs& a, hipStream_t s) {
   constexpr int most = stream_most(D, sizeof(T));
   if constexpr (sizeof(T) == 2)
     if (tiled(rows, 1)) {
-      k_attn_tile<D><<<kWg, 256, 0, s>>>(a, kWg, kGrain);
+      k_attn_tile<D><<<kWg, Tile<D>::W * kWave, 0, s>>>(a, kWg, kGrain);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      k_attn_join<T, D, kTileR, 8><<<dim3(kWg, kTileR / 8), 256, 0, s>>>(a, kWg);
+      constexpr int R = Tile<D>::R;
+      k_attn_join<T, D, R, 8><<<dim3(kWg, R / 8), 256, 0, s>>>(a, kWg);
       return hipGetLastError();
     }
   const int nt = stream_nt(rows, D, sizeof(T));
