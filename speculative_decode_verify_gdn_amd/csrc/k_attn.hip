@@ -625,19 +625,22 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 
 // ---- many query rows: the waves of a workgroup take different rows
 //
-// R = 128 rows; keys pass through LDS, 64 at a time, and every wave multiplies
-// with all of them.  Two forms, by the registers that a row's sums take:
+// Keys pass through LDS, a tile at a time, and every wave multiplies with all of
+// them.  Two forms of a wave:
 //
-// Rows32 (64 and 128 channels): 32 rows to a wave, four waves, products of
-// v_mfma_f32_32x32x16_bf16.  Result row m = 8a + 4h + r (h = lane / 32; register
-// 4a + r) stands for key 16 (a / 2) + 8h + 4 (a % 2) + r of its 32: then the eight
-// registers of a = 2s, 2s + 1 are eight consecutive keys, the operand of product
-// step s.
+// Rows32: 32 rows, products of v_mfma_f32_32x32x16_bf16.  Result row m = 8a + 4h + r
+// (h = lane / 32; register 4a + r) stands for key 16 (a / 2) + 8h + 4 (a % 2) + r of
+// its 32: then the eight registers of a = 2s, 2s + 1 are eight consecutive keys, the
+// operand of product step s.
 //
-// Rows16 (256 channels): 16 rows to a wave, eight waves, products of
-// v_mfma_f32_16x16x32_bf16 and keys in the stream kernel's order.  An operand from
-// LDS feeds half as many products, but two waves fit on a SIMD: with 32 rows their
-// sums and queries leave room for one, which waits for every load by itself.
+// Rows16: 16 rows, products of v_mfma_f32_16x16x32_bf16 and keys in the stream
+// kernel's order.  An operand from LDS feeds half as many products, but a wave's
+// sums and queries take half the registers.
+//
+// A tile of the line has 64 rows, four waves of 16, where no sequence has more;
+// else 128: four waves of 32, or with 256 channels eight of 16 (with 32 rows of 256
+// channels only one wave would fit on a SIMD, and it waits for every load by
+// itself: 289 against 235 us for 64 trees of 64 nodes, 16 query heads).
 //
 // LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
 // rows that are read together fall on different banks; values as in the cache,
@@ -648,10 +651,10 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 // One wave's products.  A lane has one row, and of a tile's keys kGroups times
 // eight consecutive ones: from kEvery * i + 8 * part on.
-template <int D>
+template <int D, int KT>
 struct Rows32 {
-  static constexpr int kRows = 32, kWaves = 4, kMinWaves = 2;
-  static constexpr int kGroups = 4, kEvery = 16;
+  static constexpr int kRows = 32;
+  static constexpr int kGroups = KT / 16, kEvery = 16;
   static constexpr int QJ = D / 16, DT = D / 32;  // score products, output tiles
   static constexpr int kQ = 16;                   // channels of a score product
   typedef floatx16 Acc;
@@ -659,11 +662,13 @@ struct Rows32 {
   static __device__ __forceinline__ int row_key(int c) {
     return 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
   }
-  // 16 rows in a row are served together: keys that differ in four bits
+  // LDS serves 16 rows at once, whose keys differ in four bits, 256 bytes (two rows
+  // of 64 channels) from each other or in the same ones: 16 different pieces.
   static __device__ __forceinline__ int swizzle(int key) {
     return D == 64 ? (key >> 1) & 7 : key & 15;
   }
-  static constexpr int kScoreTiles = 2;  // of 64 keys
+  static constexpr int kSwizzlePeriod = 16;  // keys after which it repeats
+  static constexpr int kScoreTiles = KT / 32;
   static __device__ __forceinline__ Acc mul(bf16x8 a, bf16x8 b, Acc c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -684,19 +689,21 @@ struct Rows32 {
   }
 };
 
-template <int D>
+template <int D, int KT>
 struct Rows16 {
-  static constexpr int kRows = 16, kWaves = 8, kMinWaves = 2;
-  static constexpr int kGroups = 2, kEvery = 32;
+  static constexpr int kRows = 16;
+  static constexpr int kGroups = KT / 32, kEvery = 32;
   static constexpr int QJ = D / 32, DT = D / 16;
   static constexpr int kQ = 32;
   typedef floatx4 Acc;
   static constexpr int kAcc = 4;
   static __device__ __forceinline__ int row_key(int c) { return 8 * (c >> 2) + (c & 3); }
+  // a score tile's keys differ in bits 0, 1, 3 and 4
   static __device__ __forceinline__ int swizzle(int key) {
-    return (key & 3) | (key >> 1 & 12);  // a score tile's keys differ in these
+    return D == 64 ? (key >> 1 & 1) | (key >> 2 & 6) : (key & 3) | (key >> 1 & 12);
   }
-  static constexpr int kScoreTiles = 4;
+  static constexpr int kSwizzlePeriod = 32;
+  static constexpr int kScoreTiles = KT / 16;
   static __device__ __forceinline__ Acc mul(bf16x8 a, bf16x8 b, Acc c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -708,12 +715,14 @@ struct Rows16 {
   static __device__ __forceinline__ float sum(float x) { return row_sum(x); }
 };
 
-template <int D>
+template <int D, int ROWS>
 struct Tile {
-  typedef typename std::conditional<D == 256, Rows16<D>, Rows32<D>>::type Mma;
-  static constexpr int W = Mma::kWaves;
-  static constexpr int R = Mma::kRows * W;
-  static constexpr int kKeys = 64;
+  static constexpr bool kNarrow = ROWS == 64 || D == 256;  // Rows16
+  static constexpr int R = ROWS;
+  // With 256 channels and 64 rows the tile is halved: two workgroups' LDS fit on a CU.
+  static constexpr int kKeys = D == 256 && ROWS == 64 ? 32 : 64;
+  typedef typename std::conditional<kNarrow, Rows16<D, kKeys>, Rows32<D, kKeys>>::type Mma;
+  static constexpr int W = ROWS / Mma::kRows;
   static constexpr int kPieces = D / 8;                         // 16-byte pieces of a key
   static constexpr int kLoads = kKeys * kPieces / (W * kWave);  // of a wave, K and V each
   static constexpr int kKeysPerLoad = W * kWave / kPieces;      // of the workgroup
@@ -761,10 +770,10 @@ __device__ __forceinline__ void lds_loads_done() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
 }
 
-template <int D>
-__global__ __launch_bounds__(Tile<D>::W * kWave, Tile<D>::Mma::kMinWaves) void k_attn_tile(
-    AttnArgs p, int n_wg, long long grain) {
-  using Tl = Tile<D>;
+template <int D, int ROWS>
+__global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(AttnArgs p, int n_wg,
+                                                                           long long grain) {
+  using Tl = Tile<D, ROWS>;
   using Mm = typename Tl::Mma;
   typedef typename Mm::Acc Acc;
   using F = Frag<uint16_t>;
@@ -797,9 +806,8 @@ __global__ __launch_bounds__(Tile<D>::W * kWave, Tile<D>::Mma::kMinWaves) void k
   const size_t head_sz = static_cast<size_t>(ps) * D;
   const size_t page_sz = static_cast<size_t>(p.Hkv) * head_sz;
   // The lane's offset in a load of keys: its key behind the wave's first, and the
-  // piece that belongs at its place.  With 256 channels a load of the workgroup is
-  // 16 keys, and every other one permutes differently.
-  constexpr int KP = D == 256 ? 2 : 1;
+  // piece that belongs at its place; the same for every KP-th load of the wave.
+  constexpr int KP = Mm::kSwizzlePeriod > Tl::kKeysPerLoad ? Mm::kSwizzlePeriod / Tl::kKeysPerLoad : 1;
   uint32_t k_off[KP];
 #pragma unroll
   for (int j = 0; j < KP; ++j) {
@@ -1148,10 +1156,10 @@ __global__ __launch_bounds__(Tile<D>::W * kWave, Tile<D>::Mma::kMinWaves) void k
 }
 
 // Adds the fragments of the item that workgroup blockIdx.x began and did not
-// end, in order of their keys, RB rows at a time.  Four fragments or fewer: each
-// wave takes every fourth row.  More (a long context and few rows): wave w takes
-// fragments w, w + 4, ... of every row, and the four partial results are added
-// in order.
+// end, in order of their keys.  Four fragments or fewer: a wave has RB rows, all
+// their fragments in flight at once.  More (a long context and few rows): a
+// workgroup has RB rows, wave w fragments w, w + 4, ... of each, and the four
+// partial results are added in order.
 template <int E>
 struct Partial {
   float m, l, o[E];
@@ -1177,7 +1185,8 @@ struct Partial {
 template <typename T, int D, int R, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
-  const int w0 = blockIdx.x, row0 = blockIdx.y * RB;
+  const int w0 = blockIdx.x;
+  int row0 = blockIdx.y * RB;
   const AttnJoin j = places.join[w0];
   if (j.last < 0 || row0 >= j.rows) return;
   constexpr int E = D / kWave;
@@ -1207,38 +1216,43 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
     __builtin_memcpy(__builtin_assume_aligned(out, E * sizeof(T)), e, sizeof(e));
   };
   if (n <= 4) {
-    constexpr int M = (RB + 3) / 4;
-    Partial<E> y[M][4];
+    // one workgroup of four does the rows of all: RB rows to a wave
+    if (blockIdx.y % 4 != 0) return;
+    row0 += wave * RB;
+    Partial<E> y[RB][4];
 #pragma unroll
-    for (int i = 0; i < M; ++i)
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int row = row0 + wave + 4 * i;
         y[i][f].clear();
-        if (f < n && wave + 4 * i < RB && row < j.rows) y[i][f] = load(f, row);
+        if (f < n && row0 + i < j.rows) y[i][f] = load(f, row0 + i);
       }
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const int row = row0 + wave + 4 * i;
-      if (wave + 4 * i >= RB || row >= j.rows) continue;
+    for (int i = 0; i < RB; ++i) {
+      if (row0 + i >= j.rows) continue;
 #pragma unroll
       for (int f = 1; f < 4; ++f) y[i][0].add(y[i][f], c2);
-      write(y[i][0], row);
+      write(y[i][0], row0 + i);
     }
     return;
   }
   Partial<E> acc[RB];
 #pragma unroll
   for (int i = 0; i < RB; ++i) acc[i].clear();
-  for (int f = wave; f < n; f += 4) {
-    Partial<E> y[RB];
+  constexpr int U = 16 / RB;  // fragments in flight: 16 rows of them
+  for (int f0 = wave; f0 < n; f0 += 4 * U) {
+    Partial<E> y[U][RB];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      y[i].clear();
-      if (row0 + i < j.rows) y[i] = load(f, row0 + i);
-    }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < RB; ++i) acc[i].add(y[i], c2);
+      for (int i = 0; i < RB; ++i) {
+        y[u][i].clear();
+        if (f0 + 4 * u < n && row0 + i < j.rows) y[u][i] = load(f0 + 4 * u, row0 + i);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RB; ++i) acc[i].add(y[u][i], c2);
   }
   if (wave > 0)
 #pragma unroll
@@ -1254,59 +1268,75 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   }
 }
 
-// Two workgroups per CU, each with at least kGrain keys.
-constexpr int kWg = 512;
-constexpr long long kGrain = 256;
+// A workgroup has at least this many keys (in 32 bits, where a key's products take
+// sixteen times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64).
+constexpr long long grain_of(int size) { return size == 2 ? 256 : 64; }
+constexpr int kCus = 256;
 
-constexpr int kTileR = Tile<128>::R;
-static_assert(Tile<64>::R == kTileR && Tile<256>::R == kTileR, "one workspace rule");
+// The kernel and tile for sequences of at most `rows` query rows, and how many
+// workgroups: as many as the chip holds at once.
+struct AttnPlan {
+  int tile;  // rows of the tile kernel's tile, or 0: the stream kernel
+  int nt;    // its 16s of rows
+  int wgs;
+  int rows() const { return tile ? tile : 16 * nt; }
+};
 
-// bf16 batches with more rows to a sequence than the stream kernel holds take
-// the tile kernel.
-bool tiled(long long rows, int dtype) { return dtype == 1 && rows > 64; }
-
-// Rows of a tile: the fewest 16s that hold a sequence's rows, as far as their
-// sums, a float per row and channel, stay in registers beside the operands.
-constexpr int stream_most(int head_dim, int size) {
-  const int most = size == 2 ? 512 / head_dim : 256 / head_dim;
-  return most > 4 ? 4 : most < 1 ? 1 : most;
-}
-int stream_nt(long long rows, int head_dim, int size) {
+// Rows of the stream kernel's tile in 16s: with bf16 it takes 16 rows at most, and
+// the tile kernel more (64 rows of 32 sequences of about 3,000 keys: 44 us there, 74
+// us with 64 rows' sums in one wave's registers).  In 32 bits 32 rows, as far as
+// their sums stay in registers beside the operands.
+constexpr int stream_most(int head_dim, int size) { return size == 2 || head_dim == 256 ? 1 : 2; }
+AttnPlan attn_plan(long long rows, int head_dim, int size) {
+  AttnPlan a{0, 1, 2 * kCus};
+  if (size == 2 && rows > 16) {
+    a.tile = rows > 64 ? 128 : 64;
+    return a;
+  }
   const int most = stream_most(head_dim, size);
-  const int want = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return want < most ? want : most;
+  const int want = rows <= 16 ? 1 : 2;
+  a.nt = want < most ? want : most;
+  // registers for one wave on a SIMD only
+  if (a.nt * head_dim * size > 256) a.wgs = kCus;
+  return a;
+}
+
+template <typename T, int D, int R>
+hipError_t join_t(const AttnArgs& a, int wgs, hipStream_t s) {
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr int RB = R < 64 ? R / 16 : 4;
+  const long long rows = static_cast<long long>(a.k.T) * (a.Hq / a.Hkv);
+  const int most = static_cast<int>(rows < R ? rows : R);
+  k_attn_join<T, D, R, RB><<<dim3(wgs, (most + RB - 1) / RB), 256, 0, s>>>(a, wgs);
+  return hipGetLastError();
 }
 
 template <typename T, int D, int NT>
-hipError_t stream_t(const AttnArgs& a, hipStream_t s) {
-  constexpr int R = 16 * NT;
-  k_attn_stream<T, D, NT><<<kWg, 256, 0, s>>>(a, kWg, kGrain);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  constexpr int RB = NT;  // 16 workgroups of rows
-  k_attn_join<T, D, R, RB><<<dim3(kWg, R / RB), 256, 0, s>>>(a, kWg);
-  return hipGetLastError();
+hipError_t stream_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  k_attn_stream<T, D, NT><<<p.wgs, 256, 0, s>>>(a, p.wgs, grain_of(sizeof(T)));
+  return join_t<T, D, 16 * NT>(a, p.wgs, s);
+}
+
+template <int D, int ROWS>
+hipError_t tile_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  k_attn_tile<D, ROWS><<<p.wgs, Tile<D, ROWS>::W * kWave, 0, s>>>(a, p.wgs, grain_of(2));
+  return join_t<uint16_t, D, ROWS>(a, p.wgs, s);
 }
 
 template <typename T, int D>
 hipError_t attn_t(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.k.T) * (a.Hq / a.Hkv);
-  constexpr int most = stream_most(D, sizeof(T));
-  if constexpr (sizeof(T) == 2)
-    if (tiled(rows, 1)) {
-      k_attn_tile<D><<<kWg, Tile<D>::W * kWave, 0, s>>>(a, kWg, kGrain);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      constexpr int R = Tile<D>::R;
-      k_attn_join<T, D, R, 8><<<dim3(kWg, R / 8), 256, 0, s>>>(a, kWg);
-      return hipGetLastError();
-    }
-  const int nt = stream_nt(rows, D, sizeof(T));
-  if constexpr (most >= 4)
-    if (nt == 4) return stream_t<T, D, 4>(a, s);
-  if constexpr (most >= 2)
-    if (nt == 2) return stream_t<T, D, 2>(a, s);
-  return stream_t<T, D, 1>(a, s);
+  const AttnPlan p = attn_plan(rows, D, sizeof(T));
+  if constexpr (sizeof(T) == 2) {
+    if (p.tile == 128) return tile_t<D, 128>(a, p, s);
+    if (p.tile == 64) return tile_t<D, 64>(a, p, s);
+  } else {
+    constexpr int most = stream_most(D, sizeof(T));
+    if constexpr (most >= 2)
+      if (p.nt == 2) return stream_t<T, D, 2>(a, p, s);
+  }
+  return stream_t<T, D, 1>(a, p, s);
 }
 
 }  // namespace
@@ -1326,10 +1356,10 @@ hipError_t launch_attn(const AttnArgs& a, int head_dim, int dtype, hipStream_t s
 
 size_t attn_workspace(int L, int B, int T, int N, int Hq, int Hkv, int head_dim, int dtype,
                       long long max_tokens) {
-  const long long rows = static_cast<long long>(T) * (Hq / Hkv);
-  const int R = tiled(rows, dtype) ? kTileR : 16 * stream_nt(rows, head_dim, dtype == 1 ? 2 : 4);
-  return static_cast<size_t>(2 * kWg) * R * (head_dim + 2) * sizeof(float) +
-         static_cast<size_t>(kWg) * sizeof(AttnJoin);
+  const AttnPlan p =
+      attn_plan(static_cast<long long>(T) * (Hq / Hkv), head_dim, dtype == 1 ? 2 : 4);
+  return static_cast<size_t>(2 * p.wgs) * p.rows() * (head_dim + 2) * sizeof(float) +
+         static_cast<size_t>(p.wgs) * sizeof(AttnJoin);
 }
 
 }  // namespace gdn
