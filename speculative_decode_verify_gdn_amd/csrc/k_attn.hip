@@ -181,22 +181,29 @@ __device__ bool tree_masks(const int32_t* parent, int n, TreeLds& t) {
 }
 
 // Fragments in the workspace: 2 n_wg places of R rows of D sums, then of R
-// (m, l) pairs, then n_wg descriptions for the join.
+// (m, l) pairs, then n_wg descriptions for the join.  Between places lie 256 bytes
+// more: the join reads the same row of many of them, and at a distance of a power
+// of two they would all come from one memory channel (61 to 92 us for one sequence
+// of 60,000 keys and 64 rows).
 template <int R, int D>
 struct Places {
+  static constexpr size_t kPlace = static_cast<size_t>(R) * D + 64;
   float* o;
   floatx2* ml;
   AttnJoin* join;
   __device__ __host__ Places(void* ws, int n_wg) {
     o = static_cast<float*>(ws);
-    ml = reinterpret_cast<floatx2*>(o + static_cast<size_t>(2 * n_wg) * R * D);
+    ml = reinterpret_cast<floatx2*>(o + 2 * n_wg * kPlace);
     join = reinterpret_cast<AttnJoin*>(ml + static_cast<size_t>(2 * n_wg) * R);
   }
-  static size_t bytes(int n_wg) {
-    return static_cast<size_t>(2 * n_wg) * R * (D + 2) * sizeof(float) +
-           static_cast<size_t>(n_wg) * sizeof(AttnJoin);
+  __device__ __forceinline__ float* row(int place, int r) const {
+    return o + place * kPlace + static_cast<size_t>(r) * D;
   }
 };
+size_t places_bytes(int rows, int head_dim, int n_wg) {
+  return static_cast<size_t>(2 * n_wg) * ((static_cast<size_t>(rows) * head_dim + 64) * 4 + rows * 8) +
+         static_cast<size_t>(n_wg) * sizeof(AttnJoin);
+}
 
 // What a row sees of `count` consecutive keys from `base` on, as bits: in a
 // chain the keys below lim; in a tree the cached ones (below ctx) and those of
@@ -593,8 +600,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
             for (int j = 0; j < 4; ++j) e4[j] = to_out(v[j] * inv, T{});
             __builtin_memcpy(__builtin_assume_aligned(dst, 4 * sizeof(T)), e4, sizeof(e4));
           } else {
-            *reinterpret_cast<floatx4*>(
-                &places.o[(static_cast<size_t>(place) * R + rr) * D + dd]) = v;
+            *reinterpret_cast<floatx4*>(places.row(place, rr) + dd) = v;
           }
         }
       }
@@ -1115,9 +1121,9 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
               __builtin_memcpy(__builtin_assume_aligned(dst + t * MR + 8 * a, 8), e4, 8);
             }
         } else {
-          const size_t at =
-              static_cast<size_t>(2 * wg + (it.at < st.lo ? 0 : 1)) * R + wave * MR + opaque(c);
-          if (h == 0) places.ml[at] = floatx2{m, l};
+          const int place = 2 * wg + (it.at < st.lo ? 0 : 1), row = wave * MR + opaque(c);
+          if (h == 0) places.ml[static_cast<size_t>(place) * R + row] = floatx2{m, l};
+          float* const dst = places.row(place, row) + 4 * h;
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1125,7 +1131,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
               floatx4 v;
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[i] = o[t][4 * a + i];
-              *reinterpret_cast<floatx4*>(&places.o[at * D + t * MR + 8 * a + 4 * h]) = v;
+              *reinterpret_cast<floatx4*>(dst + t * MR + 8 * a) = v;
             }
         }
       }
@@ -1182,6 +1188,8 @@ struct Partial {
   }
 };
 
+constexpr int kMostWg = 512;
+
 template <typename T, int D, int R, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
@@ -1190,19 +1198,20 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const AttnJoin j = places.join[w0];
   if (j.last < 0 || row0 >= j.rows) return;
   constexpr int E = D / kWave;
-  __shared__ Partial<E> sh[3][RB][kWave];
+  __shared__ float weight[RB][kMostWg];  // of a fragment, over l of them all
+  __shared__ float part[3][RB][D];
   const int lane = threadIdx.x % kWave, wave = uni(static_cast<int>(threadIdx.x) / kWave);
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
   const float inv_g = 1.f / static_cast<float>(p.Hq / p.Hkv);
   const int n = j.last - w0 + 1;
   auto load = [&](int f, int row) {  // fragment f of a row that is there
     Partial<E> y;
-    const size_t at = static_cast<size_t>(2 * (w0 + f) + (f == 0 ? 1 : 0)) * R + row;
-    const floatx2 ml = places.ml[at];
+    const int place = 2 * (w0 + f) + (f == 0 ? 1 : 0);
+    const floatx2 ml = places.ml[static_cast<size_t>(place) * R + row];
     y.m = ml[0];
     y.l = ml[1];
 #pragma unroll
-    for (int i = 0; i < E; ++i) y.o[i] = places.o[at * D + lane * E + i];
+    for (int i = 0; i < E; ++i) y.o[i] = places.row(place, row)[lane * E + i];
     return y;
   };
   auto write = [&](const Partial<E>& y, int row) {
@@ -1236,35 +1245,60 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
     }
     return;
   }
-  Partial<E> acc[RB];
+  // the weights first, a lane to a fragment, so that the long sums wait for loads only
+  auto place = [&](int f) { return 2 * (w0 + f) + (f == 0 ? 1 : 0); };
+  for (int i = wave; i < RB; i += 4) {
+    const floatx2* ml = places.ml + min(row0 + i, j.rows - 1);
+    float M = kNegInf;
+    for (int f = lane; f < n; f += kWave) M = fmaxf(M, ml[static_cast<size_t>(place(f)) * R][0]);
 #pragma unroll
-  for (int i = 0; i < RB; ++i) acc[i].clear();
-  constexpr int U = 16 / RB;  // fragments in flight: 16 rows of them
-  for (int f0 = wave; f0 < n; f0 += 4 * U) {
-    Partial<E> y[U][RB];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        y[u][i].clear();
-        if (f0 + 4 * u < n && row0 + i < j.rows) y[u][i] = load(f0 + 4 * u, row0 + i);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < RB; ++i) acc[i].add(y[u][i], c2);
+    for (int off = 32; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, kWave));
+    float L = 0.f;
+    for (int f = lane; f < n; f += kWave) {
+      const floatx2 y = ml[static_cast<size_t>(place(f)) * R];
+      // a fragment without keys has no weight; l may be NaN where m is still -inf
+      const float w = y[0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((y[0] - M) * c2);
+      if (w != 0.f || y[1] != y[1]) L += y[1] == y[1] ? y[1] * w : y[1];
+      weight[i][f] = w;
+    }
+    L = wave_sum(L);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    for (int f = lane; f < n; f += kWave) weight[i][f] *= inv;
   }
+  __syncthreads();
+  float o[RB][E] = {};
+#pragma unroll 2
+  for (int f = wave; f < n; f += 4)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const float* from = places.row(place(f), min(row0 + i, j.rows - 1));
+      const float w = weight[i][f];
+      // a sum of no weight is left out: it may be an infinity, or never written
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float v = from[lane * E + e];
+        o[i][e] += w == 0.f ? 0.f : v * w;
+      }
+    }
   if (wave > 0)
 #pragma unroll
-    for (int i = 0; i < RB; ++i) sh[wave - 1][i][lane] = acc[i];
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[wave - 1][i][lane * E + e] = o[i][e];
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
     if (row0 + i >= j.rows) continue;
+    Partial<E> y;
+    y.l = 1.f;
 #pragma unroll
-    for (int w = 0; w < 3; ++w) acc[i].add(sh[w][i][lane], c2);
-    write(acc[i], row0 + i);
+    for (int e = 0; e < E; ++e) {
+      y.o[e] = o[i][e];
+#pragma unroll
+      for (int w = 0; w < 3; ++w) y.o[e] += part[w][i][lane * E + e];
+    }
+    write(y, row0 + i);
   }
 }
 
@@ -1288,6 +1322,7 @@ struct AttnPlan {
 // their sums stay in registers beside the operands.
 constexpr int stream_most(int head_dim, int size) { return size == 2 || head_dim == 256 ? 1 : 2; }
 AttnPlan attn_plan(long long rows, int head_dim, int size) {
+  static_assert(2 * kCus <= kMostWg, "the join's weights");
   AttnPlan a{0, 1, 2 * kCus};
   if (size == 2 && rows > 16) {
     a.tile = rows > 64 ? 128 : 64;
@@ -1358,8 +1393,7 @@ size_t attn_workspace(int L, int B, int T, int N, int Hq, int Hkv, int head_dim,
                       long long max_tokens) {
   const AttnPlan p =
       attn_plan(static_cast<long long>(T) * (Hq / Hkv), head_dim, dtype == 1 ? 2 : 4);
-  return static_cast<size_t>(2 * p.wgs) * p.rows() * (head_dim + 2) * sizeof(float) +
-         static_cast<size_t>(p.wgs) * sizeof(AttnJoin);
+  return places_bytes(p.rows(), head_dim, p.wgs);
 }
 
 }  // namespace gdn
