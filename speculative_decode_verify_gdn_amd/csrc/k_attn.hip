@@ -1189,116 +1189,156 @@ struct Partial {
 };
 
 constexpr int kMostWg = 512;
+constexpr int kFew = 4;
+constexpr int kJoinWg = 1024;  // workgroups, all resident at once
 
+// The tasks (an item's RB or 4 RB rows) are counted by every workgroup for itself
+// from the n_wg descriptions, and dealt out in turn: a grid of n_wg by rows, most
+// of which have nothing to do, costs more than that (7 against 3 us).
 template <typename T, int D, int R, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
-  const int w0 = blockIdx.x;
-  int row0 = blockIdx.y * RB;
-  const AttnJoin j = places.join[w0];
-  if (j.last < 0 || row0 >= j.rows) return;
   constexpr int E = D / kWave;
   __shared__ float weight[RB][kMostWg];  // of a fragment, over l of them all
   __shared__ float part[3][RB][D];
-  const int lane = threadIdx.x % kWave, wave = uni(static_cast<int>(threadIdx.x) / kWave);
+  __shared__ int upto[kMostWg];  // tasks of the items that workgroups 0 .. w began
+  __shared__ int wave_sum_[2][4];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = uni(tid / kWave);
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
   const float inv_g = 1.f / static_cast<float>(p.Hq / p.Hkv);
-  const int n = j.last - w0 + 1;
-  auto load = [&](int f, int row) {  // fragment f of a row that is there
-    Partial<E> y;
-    const int place = 2 * (w0 + f) + (f == 0 ? 1 : 0);
-    const floatx2 ml = places.ml[static_cast<size_t>(place) * R + row];
-    y.m = ml[0];
-    y.l = ml[1];
+  int scan[2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) y.o[i] = places.row(place, row)[lane * E + i];
-    return y;
-  };
-  auto write = [&](const Partial<E>& y, int row) {
-    const int G = p.Hq / p.Hkv, tok = tile_token(j.skip, row, inv_g);
-    T* out = static_cast<T*>(p.o) + j.out +
-             (static_cast<long long>(tok) * p.Hq + j.skip + row - tok * G) * D + lane * E;
-    const float inv = y.l == 0.f ? 0.f : 1.f / y.l;
-    T e[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) e[i] = to_out(y.o[i] * inv, T{});
-    __builtin_memcpy(__builtin_assume_aligned(out, E * sizeof(T)), e, sizeof(e));
-  };
-  if (n <= 4) {
-    // one workgroup of four does the rows of all: RB rows to a wave
-    if (blockIdx.y % 4 != 0) return;
-    row0 += wave * RB;
-    Partial<E> y[RB][4];
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        y[i][f].clear();
-        if (f < n && row0 + i < j.rows) y[i][f] = load(f, row0 + i);
+  for (int i = 0; i < 2; ++i) {
+    const int w = i * 256 + tid;
+    int tasks = 0;
+    if (w < n_wg) {
+      const AttnJoin j = places.join[w];
+      if (j.last >= 0) {
+        const int per = j.last - w + 1 <= kFew ? 4 * RB : RB;
+        tasks = (j.rows + per - 1) / per;
       }
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      if (row0 + i >= j.rows) continue;
-#pragma unroll
-      for (int f = 1; f < 4; ++f) y[i][0].add(y[i][f], c2);
-      write(y[i][0], row0 + i);
     }
-    return;
-  }
-  // the weights first, a lane to a fragment, so that the long sums wait for loads only
-  auto place = [&](int f) { return 2 * (w0 + f) + (f == 0 ? 1 : 0); };
-  for (int i = wave; i < RB; i += 4) {
-    const floatx2* ml = places.ml + min(row0 + i, j.rows - 1);
-    float M = kNegInf;
-    for (int f = lane; f < n; f += kWave) M = fmaxf(M, ml[static_cast<size_t>(place(f)) * R][0]);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, kWave));
-    float L = 0.f;
-    for (int f = lane; f < n; f += kWave) {
-      const floatx2 y = ml[static_cast<size_t>(place(f)) * R];
-      // a fragment without keys has no weight; l may be NaN where m is still -inf
-      const float w = y[0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((y[0] - M) * c2);
-      if (w != 0.f || y[1] != y[1]) L += y[1] == y[1] ? y[1] * w : y[1];
-      weight[i][f] = w;
-    }
-    L = wave_sum(L);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int f = lane; f < n; f += kWave) weight[i][f] *= inv;
+    scan[i] = static_cast<int>(wave_scan(tasks));
+    if (lane == kWave - 1) wave_sum_[i][wave] = scan[i];
   }
   __syncthreads();
-  float o[RB][E] = {};
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w == wave) upto[i * 256 + tid] = before + scan[i];
+      before += wave_sum_[i][w];
+    }
+  __syncthreads();
+  for (int task = blockIdx.x; task < before; task += gridDim.x) {
+    int w0 = 0, hi = kMostWg - 1;  // the first with more tasks up to it
+    while (w0 < hi) {
+      const int mid = (w0 + hi) / 2;
+      if (upto[mid] > task)
+        hi = mid;
+      else
+        w0 = mid + 1;
+    }
+    w0 = uni(w0);
+    const AttnJoin j = places.join[w0];
+    const int n = j.last - w0 + 1;
+    const bool few = n <= kFew;
+    int row0 = (task - (w0 ? upto[w0 - 1] : 0)) * (few ? 4 * RB : RB);
+    auto place = [&](int f) { return 2 * (w0 + f) + (f == 0 ? 1 : 0); };
+    auto load = [&](int f, int row) {  // fragment f of a row that is there
+      Partial<E> y;
+      const floatx2 ml = places.ml[static_cast<size_t>(place(f)) * R + row];
+      y.m = ml[0];
+      y.l = ml[1];
+#pragma unroll
+      for (int i = 0; i < E; ++i) y.o[i] = places.row(place(f), row)[lane * E + i];
+      return y;
+    };
+    auto write = [&](const Partial<E>& y, int row) {
+      const int G = p.Hq / p.Hkv, tok = tile_token(j.skip, row, inv_g);
+      T* out = static_cast<T*>(p.o) + j.out +
+               (static_cast<long long>(tok) * p.Hq + j.skip + row - tok * G) * D + lane * E;
+      const float inv = y.l == 0.f ? 0.f : 1.f / y.l;
+      T e[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = to_out(y.o[i] * inv, T{});
+      __builtin_memcpy(__builtin_assume_aligned(out, E * sizeof(T)), e, sizeof(e));
+    };
+    if (few) {
+      row0 += wave * RB;
+      Partial<E> y[RB][kFew];
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int f = 0; f < kFew; ++f) {
+          y[i][f].clear();
+          if (f < n && row0 + i < j.rows) y[i][f] = load(f, row0 + i);
+        }
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        if (row0 + i >= j.rows) continue;
+#pragma unroll
+        for (int f = 1; f < kFew; ++f) y[i][0].add(y[i][f], c2);
+        write(y[i][0], row0 + i);
+      }
+      continue;
+    }
+    // the weights first, a lane to a fragment, so that the long sums wait for loads only
+    for (int i = wave; i < RB; i += 4) {
+      const floatx2* ml = places.ml + min(row0 + i, j.rows - 1);
+      float M = kNegInf;
+      for (int f = lane; f < n; f += kWave) M = fmaxf(M, ml[static_cast<size_t>(place(f)) * R][0]);
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, kWave));
+      float L = 0.f;
+      for (int f = lane; f < n; f += kWave) {
+        const floatx2 y = ml[static_cast<size_t>(place(f)) * R];
+        // a fragment without keys has no weight; l may be NaN where m is still -inf
+        const float w = y[0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((y[0] - M) * c2);
+        if (w != 0.f || y[1] != y[1]) L += y[1] == y[1] ? y[1] * w : y[1];
+        weight[i][f] = w;
+      }
+      L = wave_sum(L);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      for (int f = lane; f < n; f += kWave) weight[i][f] *= inv;
+    }
+    __syncthreads();
+    float o[RB][E] = {};
 #pragma unroll 2
-  for (int f = wave; f < n; f += 4)
+    for (int f = wave; f < n; f += 4)
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const float* from = places.row(place(f), min(row0 + i, j.rows - 1));
-      const float w = weight[i][f];
-      // a sum of no weight is left out: it may be an infinity, or never written
+      for (int i = 0; i < RB; ++i) {
+        const float* from = places.row(place(f), min(row0 + i, j.rows - 1));
+        const float w = weight[i][f];
+        // a sum of no weight is left out: it may be an infinity, or never written
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float v = from[lane * E + e];
-        o[i][e] += w == 0.f ? 0.f : v * w;
+        for (int e = 0; e < E; ++e) {
+          const float v = from[lane * E + e];
+          o[i][e] += w == 0.f ? 0.f : v * w;
+        }
       }
-    }
-  if (wave > 0)
+    if (wave > 0)
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+      for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int e = 0; e < E; ++e) part[wave - 1][i][lane * E + e] = o[i][e];
-  __syncthreads();
-  if (wave > 0) return;
+        for (int e = 0; e < E; ++e) part[wave - 1][i][lane * E + e] = o[i][e];
+    __syncthreads();
+    if (wave == 0)
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    if (row0 + i >= j.rows) continue;
-    Partial<E> y;
-    y.l = 1.f;
+      for (int i = 0; i < RB; ++i) {
+        if (row0 + i >= j.rows) continue;
+        Partial<E> y;
+        y.l = 1.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      y.o[e] = o[i][e];
+        for (int e = 0; e < E; ++e) {
+          y.o[e] = o[i][e];
 #pragma unroll
-      for (int w = 0; w < 3; ++w) y.o[e] += part[w][i][lane * E + e];
-    }
-    write(y, row0 + i);
+          for (int w = 0; w < 3; ++w) y.o[e] += part[w][i][lane * E + e];
+        }
+        write(y, row0 + i);
+      }
+    __syncthreads();  // the LDS is free for the next task
   }
 }
 
@@ -1306,6 +1346,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
 // sixteen times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64).
 constexpr long long grain_of(int size) { return size == 2 ? 256 : 64; }
 constexpr int kCus = 256;
+static_assert(2 * kCus <= kMostWg, "the join counts no more");
 
 // The kernel and tile for sequences of at most `rows` query rows, and how many
 // workgroups: as many as the chip holds at once.
@@ -1322,8 +1363,7 @@ struct AttnPlan {
 // their sums stay in registers beside the operands.
 constexpr int stream_most(int head_dim, int size) { return size == 2 || head_dim == 256 ? 1 : 2; }
 AttnPlan attn_plan(long long rows, int head_dim, int size) {
-  static_assert(2 * kCus <= kMostWg, "the join's weights");
-  AttnPlan a{0, 1, 2 * kCus};
+    AttnPlan a{0, 1, 2 * kCus};
   if (size == 2 && rows > 16) {
     a.tile = rows > 64 ? 128 : 64;
     return a;
@@ -1341,9 +1381,7 @@ hipError_t join_t(const AttnArgs& a, int wgs, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int RB = R < 64 ? R / 16 : 4;
-  const long long rows = static_cast<long long>(a.k.T) * (a.Hq / a.Hkv);
-  const int most = static_cast<int>(rows < R ? rows : R);
-  k_attn_join<T, D, R, RB><<<dim3(wgs, (most + RB - 1) / RB), 256, 0, s>>>(a, wgs);
+  k_attn_join<T, D, R, RB><<<kJoinWg, 256, 0, s>>>(a, wgs);
   return hipGetLastError();
 }
 
