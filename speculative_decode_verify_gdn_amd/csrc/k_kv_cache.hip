@@ -185,36 +185,59 @@ __global__ __launch_bounds__(kNT) void k_kv_append(KvAppendArgs p) {
 // One workgroup per (sequence, layer) puts the accepted path's rows into the
 // slots of the first tokens, read from the round's k and v, so that no copy
 // depends on another; one more workgroup counts lengths and pages.  The two
-// touch nothing in common.
+// touch nothing in common.  A wave has several rows of a head on their way at once.
+// A row of k is a few 16-byte pieces, a lane each.  A row of v lies in the cache with
+// 8 slots between two channels, so neighbouring lanes take neighbouring channels
+// and a store touches as few lines as it can.
 template <typename T, int D>
 __device__ void commit_rows(const KvCommitArgs& p, int b, int l) {
+  constexpr int E = 16 / sizeof(T);   // elements of a piece
+  constexpr int P = D / E;            // pieces of a row
+  constexpr int RW = kWave / P;       // rows of a wave
+  constexpr int C = D / kWave;        // channels of v of a lane
   const KvBatch& k = p.k;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const KvSpan r = kv_rows(k, b);
   const int n = p.n_keep[b];
   if (n <= 0 || n > r.n) return;  // n <= T <= 64: a wave holds the path
   int node = lane < n ? p.path[static_cast<size_t>(b) * k.T + lane] : 0;
+  int slot = lane < n ? p.slots[r.s + lane] : -1;
   if (__any(node < 0 || node >= r.n)) return;
-  const int slot = lane < n ? p.slots[r.s + lane] : -1;
-  const int total = k.n_pages << k.page_shift, ps = 1 << k.page_shift;
+  if (slot >= k.n_pages << k.page_shift) slot = -1;
+  const int ps = 1 << k.page_shift;
   const size_t head = static_cast<size_t>(ps) * D;
   const size_t layer = static_cast<size_t>(l) * k.n_pages * p.H * head;
   const T* kk = static_cast<const T*>(p.kk) + static_cast<size_t>(l) * k.N * p.k_ld;
   const T* vv = static_cast<const T*>(p.vv) + static_cast<size_t>(l) * k.N * p.v_ld;
-  for (int i = wave; i < n * p.H; i += kNT / kWave) {
-    const int t = i / p.H, h = i % p.H;
-    const int from = __shfl(node, t, kWave), s = __shfl(slot, t, kWave);
-    if (from == t || s < 0 || s >= total) continue;  // in place already
-    const int off = s & (ps - 1);
-    const size_t page = layer + (static_cast<size_t>(s >> k.page_shift) * p.H + h) * head;
-    T* kd = static_cast<T*>(p.k_cache) + page + static_cast<size_t>(off) * D;
-    T* vd = static_cast<T*>(p.v_cache) + page + static_cast<size_t>(off / 8) * (D * 8) + off % 8;
-    const T* ks = kk + static_cast<size_t>(r.s + from) * p.k_ld + h * D;
-    const T* vs = vv + static_cast<size_t>(r.s + from) * p.v_ld + h * D;
+  T* kc = static_cast<T*>(p.k_cache) + layer;
+  T* vc = static_cast<T*>(p.v_cache) + layer;
+  const int c = lane % P * E, rows = n * p.H;
+  for (int i0 = wave * RW; i0 < rows; i0 += kNT / kWave * RW) {
+    T vx[RW][C];
 #pragma unroll
-    for (int d = lane; d < D; d += kWave) {
-      kd[d] = ks[d];
-      vd[d * 8] = vs[d];
+    for (int j = 0; j < RW; ++j) {
+      const int i = min(i0 + j, rows - 1), h = i / n;
+      const int from = __shfl(node, i - h * n, kWave);
+      const T* src = vv + (r.s + from) * p.v_ld + h * D + lane * C;
+#pragma unroll
+      for (int e = 0; e < C; ++e) vx[j][e] = src[e];
+    }
+    const int i = min(i0 + lane / P, rows - 1), h = i / n;  // the last row may be done twice
+    const int from = __shfl(node, i - h * n, kWave), s = __shfl(slot, i - h * n, kWave);
+    const u32x4 kx = *reinterpret_cast<const u32x4*>(kk + (r.s + from) * p.k_ld + h * D + c);
+    if (s >= 0)
+      *reinterpret_cast<u32x4*>(kc + (static_cast<size_t>(s >> k.page_shift) * p.H + h) * head +
+                                static_cast<size_t>(s & (ps - 1)) * D + c) = kx;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      const int i = min(i0 + j, rows - 1), h = i / n;
+      const int s = __shfl(slot, i - h * n, kWave);
+      if (s < 0) continue;
+      const int off = s & (ps - 1);
+      T* dst = vc + (static_cast<size_t>(s >> k.page_shift) * p.H + h) * head +
+               static_cast<size_t>(off / 8) * (D * 8) + off % 8 + lane * C * 8;
+#pragma unroll
+      for (int e = 0; e < C; ++e) dst[e * 8] = vx[j][e];
     }
   }
 }
@@ -247,14 +270,20 @@ __device__ void commit_counts(const KvCommitArgs& p) {
           if (keep > 0) err |= GDN_DEV_ERR_NO_PAGES;
           keep = 0;
         }
-        if (p.path)
-          for (int i = 0; i < keep; ++i) {
-            const int node = p.path[static_cast<size_t>(b) * k.T + i];
-            if (node < 0 || node >= r.n) {
-              err |= GDN_DEV_ERR_PATH;
-              keep = 0;
+        if (p.path) {
+          const int32_t* path = p.path + static_cast<size_t>(b) * k.T;
+          bool bad = false;
+          for (int i = 0; i < keep; i += 8)  // loads that wait for no other
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int node = path[min(i + j, keep - 1)];
+              bad |= node < 0 || node >= r.n;
             }
+          if (bad) {
+            err |= GDN_DEV_ERR_PATH;
+            keep = 0;
           }
+        }
       }
       if (r.ok) {
         const bool ends = p.done && p.done[b] != 0;
@@ -268,23 +297,26 @@ __device__ void commit_counts(const KvCommitArgs& p) {
     }
     long long total;
     const long long upto = block_scan(to - from, lds, total);
-    const long long at = top + upto - (to - from);
-    // a wave writes each of its sequences' pages together: a sequence that
-    // ends may hold thousands
-    for (unsigned long long m = __ballot(to > from); m; m &= m - 1) {
-      const int who = __builtin_ctzll(m);
-      const int f = __shfl(from, who, kWave), e = __shfl(to, who, kWave);
-      const long long dst = __shfl(at, who, kWave);
-      const int32_t* row =
-          p.block_table + static_cast<size_t>(c + tid - lane + who) * k.max_blocks;
-      for (int j = f + lane; j < e; j += kWave) {
-        const int pg = row[j];
-        if (pg < 0 || pg >= k.n_pages) err |= GDN_DEV_ERR_PAGE;
-        if (dst + j - f < k.n_pages)
-          p.free_pages[dst + j - f] = pg;
-        else
-          err |= GDN_DEV_ERR_NO_PAGES;
-      }
+    // a wave deals its sequences' pages out to its lanes, one each at a time:
+    // sixty-four trees give one or two pages each, a sequence that ends thousands
+    // (64 trees of 64 tokens, ten layers: a sequence at a time 25 us, so 12 us)
+    const long long first = __shfl(upto - (to - from), 0, kWave);  // of the wave
+    const long long mine = upto - first, all = __shfl(mine, kWave - 1, kWave);
+    for (long long q0 = 0; q0 < all; q0 += kWave) {
+      const long long q = min(q0 + lane, all - 1);  // the last page may be done twice
+      int who = 0;  // the first sequence whose pages end behind q
+#pragma unroll
+      for (int step = kWave / 2; step; step /= 2)
+        if (__shfl(mine, who + step - 1, kWave) <= q) who += step;
+      const int e = __shfl(to, who, kWave);
+      const long long end = __shfl(mine, who, kWave);
+      const int j = e - static_cast<int>(end - q);
+      const int pg = p.block_table[static_cast<size_t>(c + tid - lane + who) * k.max_blocks + j];
+      if (pg < 0 || pg >= k.n_pages) err |= GDN_DEV_ERR_PAGE;
+      if (top + first + q < k.n_pages)
+        p.free_pages[top + first + q] = pg;
+      else
+        err |= GDN_DEV_ERR_NO_PAGES;
     }
     top += total;
   }

@@ -372,6 +372,22 @@ def test_commit_chain_shaped_long_paths_and_repeats():
     check_commit(bt, np.array([64, 40]), path, None)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_commit_writes_every_kept_row(dtype):
+    """Kept rows come from k and v, also those whose place is their own, whatever
+    the cache holds there."""
+    bt = R.Batch(85, [7, 30], [9, 12], L=2, Hq=4, Hkv=4, D=128, dtype=dtype)
+    table, slots, left = check_reserve(bt)
+    path = np.full((2, 12), -1, np.int64)
+    path[0, :4], path[1, :3] = [0, 1, 5, 8], [0, 2, 3]
+    keep = np.array([4, 3])
+    bt.g_commit(keep, path, None)
+    _, _, _, kc, vc, err = bt.r_commit(keep, path, None, slots, table, bt.free, left, bt.kc, bt.vc)
+    assert int(bt.d["err"]) == err == 0
+    same(R.hostf(bt.d["kc"]), kc, "k cache")
+    same(R.hostf(bt.d["vc"]), vc, "v cache")
+
+
 def test_commit_errors():
     bt = R.Batch(83, [7, 30, 2, 9], [10, 20, 5, 4])
     path = np.tile(np.arange(20), (4, 1)).astype(np.int64)
