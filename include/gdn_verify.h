@@ -397,9 +397,9 @@ gdn_status gdn_conv_state_rollback(const gdn_shape* shape, int32_t T, void* conv
  * n_q_heads % n_kv_heads == 0; F32 or BF16; n_pages * page_size < 2^31;
  * max_blocks * page_size <= 2^30; batch < 65536; n_q_heads < 65536; n_layers *
  * n_kv_heads < 65536; n_layers * batch <= 2^23; n_tokens <= 2^24, and for
- * attn_verify n_tokens * n_q_heads / n_kv_heads <= 2^30.  A sequence whose lengths are malformed
- * (q_start decreasing or outside [0, n_tokens], more than T new tokens,
- * seq_len < 0, seq_len + new > max_blocks * page_size) sets
+ * attn_verify n_tokens * n_q_heads / n_kv_heads <= 2^30.  A sequence whose
+ * lengths are malformed (q_start decreasing or outside [0, n_tokens], more than
+ * T new tokens, seq_len < 0, seq_len + new > max_blocks * page_size) sets
  * GDN_DEV_ERR_LENGTH and is left out.
  */
 typedef struct {
@@ -462,7 +462,8 @@ gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int
  *   o           [L,n_tokens,Hq,D] contiguous, dtype of q
  *   seq_len     [B] int32: cached tokens before the new ones
  *   block_table [B,max_blocks] as kv_reserve left it
- *   scale       finite; 1/sqrt(D) in most models
+ *   scale       finite, and so log2(e) times it; 1/sqrt(D) in most models.  The
+ *               scores, scaled and not, are to lie within fp32's range
  *   workspace   device scratch of attn_verify_workspace_bytes(shape, T,
  *               n_tokens), 16-byte aligned; calls that may overlap need one
  *               each
@@ -470,10 +471,12 @@ gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int
  * with bf16 the probabilities are rounded to bf16 for the product with V.
  * Cache places behind a sequence's last token may hold anything, NaN included.
  * So may masked new tokens: an infinite or NaN value (or key) of a token
- * reaches only the rows that attend to it.  A malformed parent array sets
+ * reaches only the rows that attend to it.  A score of -inf counts for nothing;
+ * a row all of whose scores are such is 0.  A malformed parent array sets
  * GDN_DEV_ERR_PARENT and leaves the sequence's rows of o unwritten.  A page
  * number outside the pool sets GDN_DEV_ERR_PAGE; its tokens then count as
- * masked, and the rows of that sequence are meaningless.  The result is the same bit for bit from call to call.
+ * masked, and the rows of that sequence are meaningless.  The result is the same
+ * bit for bit from call to call.
  */
 gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const int32_t* q_start,
                        const int32_t* seq_len, const int32_t* block_table, const int32_t* parent,
@@ -500,8 +503,9 @@ size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_t
  *           n_left entries, in order of sequence, then of block
  * n_keep outside [0, new tokens] sets GDN_DEV_ERR_N_KEEP and a path entry
  * outside them GDN_DEV_ERR_PATH; of such a sequence nothing is kept.  Nothing
- * is kept or given back of a sequence that kv_reserve did not serve (first
- * slot -1); n_keep > 0 then sets GDN_DEV_ERR_NO_PAGES.  With path NULL, k, v
+ * is kept of a sequence that kv_reserve did not serve (first slot -1); n_keep > 0
+ * then sets GDN_DEV_ERR_NO_PAGES.  It has no new pages to give back, and its old
+ * ones go only with done.  With path NULL, k, v
  * and the caches are not used and may be NULL.
  * Source: GDN page s4 (the window rebuilt from the accepted raw tokens), for
  * the attention layers' cache.

@@ -155,7 +155,7 @@ gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const
   const gdn_status st = check_batch(shape, T, n_tokens, q_start);
   if (st != GDN_OK) return st;
   if (!seq_len || !block_table || !q || !k_cache || !v_cache || !o) return GDN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * 1.4426950408889634f)) return GDN_ERR_INVALID_ARG;  // exp2's factor
   if (!ld_ok(shape, q_ld, shape->n_q_heads)) return GDN_ERR_INVALID_ARG;
   if (!aligned(q) || !aligned(k_cache) || !aligned(v_cache) || !aligned(o))
     return GDN_ERR_INVALID_ARG;

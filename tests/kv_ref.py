@@ -146,16 +146,18 @@ def attend(sh, T, N, q_start, seq_len, table, parent, q, scale, kc, vc, o):
             for h in range(sh.Hkv):
                 K = kc[l, pg, h, off].astype(np.float64)
                 V = vc[l, pg, h, off // 8, :, off % 8].astype(np.float64)
+                aK, aV = np.abs(K), np.abs(V)
                 for i in range(n):
-                    w = live[i]
+                    w = live[i] if parent is not None else slice(0, c + i + 1)
                     Q = q[l, s + i, h * G:(h + 1) * G].astype(np.float64)
                     z = scale * (Q @ K[w].T)
                     p = np.exp(z - z.max(-1, keepdims=True))
                     p /= p.sum(-1, keepdims=True)
                     res = p @ V[w]
-                    Z = (abs(scale) * (np.abs(Q) @ np.abs(K[w]).T)).max()
-                    rel = 2 * ((sh.D + 2 + 6) * 2.0 ** -24 * Z + 2.0 ** -22) + 4 * w.sum() * 2.0 ** -24
-                    A = p @ np.abs(V[w])
+                    Z = abs(scale) * (np.abs(Q) @ aK[w].T)
+                    Z = Z[np.isfinite(Z)].max(initial=0.0)  # scores of -inf count for nothing
+                    rel = 2 * ((sh.D + 2 + 6) * 2.0 ** -24 * Z + 2.0 ** -22) + 4 * p.shape[1] * 2.0 ** -24
+                    A = p @ aV[w]
                     t = A * (rel + (2.0 ** -8 if bf16 else 0.0))
                     o[l, s + i, h * G:(h + 1) * G] = res
                     tol[l, s + i, h * G:(h + 1) * G] = t + (2.0 ** -8 if bf16 else 2.0 ** -24) * (np.abs(res) + t)

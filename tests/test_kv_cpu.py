@@ -110,7 +110,7 @@ def test_attention_refusals(lib):
         assert call(**{"a%d" % i: None}) == gb.GDN_ERR_INVALID_ARG
     for i in (7, 10, 11, 12):
         assert call(**{"a%d" % i: ODD}) == gb.GDN_ERR_INVALID_ARG
-    for x in (float("nan"), float("inf"), -float("inf")):
+    for x in (float("nan"), float("inf"), -float("inf"), 3e38, -3e38):
         assert call(a9=x) == gb.GDN_ERR_INVALID_ARG
     assert call(a8=255) == gb.GDN_ERR_INVALID_ARG
     assert call(a8=260) == gb.GDN_ERR_INVALID_ARG

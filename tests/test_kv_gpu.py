@@ -300,6 +300,150 @@ def test_attention_bad_page_numbers(T):
     assert int(bt.d["err"]) == gb.DEV_ERR_PAGE | gb.DEV_ERR_LENGTH
 
 
+@pytest.mark.parametrize("B", [64, 65, 130, 300])
+@pytest.mark.parametrize("Hq,T", [(4, 3), (16, 3), (16, 9)])
+def test_attention_many_sequences(Hq, T, B):
+    """More sequences than a wave or a workgroup has lanes, some of no tokens;
+    rows of up to 16, 64 and 128 to a key head."""
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, T + 1, B).tolist()
+    new[0], new[-1] = 0, T
+    check_attention(R.Batch(90 + B, rng.integers(0, 90, B).tolist(), new, Hq=Hq, Hkv=1, pad=3))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,T,tree", [(4, 3, False), (8, 7, True), (8, 30, True), (2, 150, False)])
+def test_attention_rows_shared_by_many_workgroups(Hq, T, tree, D, dtype):
+    """Contexts long enough to be split, for every size of a row tile, between
+    sequences that begin and end inside a workgroup's part."""
+    check_attention(R.Batch(91, [40, 5000, 0, 2300], [T, T, 1, T], Hq=Hq, Hkv=1, D=D, dtype=dtype,
+                            tree=tree, page=64))
+
+
+@pytest.mark.parametrize("Hq,T,tree", [(4, 3, False), (4, 3, True), (8, 7, True), (8, 40, True),
+                                       (2, 150, False)])
+def test_attention_split_rows_with_nan_and_infinities(Hq, T, tree):
+    bt = R.Batch(92, [4000, 30], [T, T], Hq=Hq, Hkv=1, D=128, tree=tree)
+    a, c = bt.q_start[0] + T - 1, bt.q_start[1] + 1
+    bt.v[:, a, :, 5], bt.v[:, a, :, 6] = np.inf, np.nan
+    bt.k[:, c, 0, 3] = np.nan
+    bt.v[:, c, 0, 9] = -np.inf
+    bt.upload()
+    table, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    bt.g_attend()
+    with np.errstate(all="ignore"):
+        want, tol = bt.r_attend(table, kc, vc)
+    close(R.hostf(bt.d["o"]).astype(np.float64), want, np.where(np.isfinite(want), tol, 0.0), "o")
+    assert np.isnan(want).any() and np.isfinite(want).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [2, 12, 100])
+def test_attention_keys_whose_scores_are_infinite(T, dtype):
+    """Scores of minus infinity count for nothing, also where they come first and
+    fill more than a tile; one of plus infinity makes its row NaN."""
+    bt = R.Batch(93, [400, 90], [T, T], Hq=8, Hkv=2, D=64, dtype=dtype)
+    bt.q[..., 3] = np.abs(bt.q[..., 3]) + 0.5
+    for b, n in ((0, 150), (1, 20)):
+        for j in range(n):
+            bt.kc[:, bt.table[b, j // 16], 0, j % 16, 3] = -np.inf
+    bt.kc[:, bt.table[1, 4], 1, 5, 3] = np.inf
+    bt.upload()
+    table, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    bt.g_attend()
+    with np.errstate(all="ignore"):
+        want, tol = bt.r_attend(table, kc, vc)
+    tol = np.where(np.isfinite(want), tol, 0.0)
+    close(R.hostf(bt.d["o"]).astype(np.float64), want, tol, "o")
+    assert np.isnan(want[:, bt.q_start[1]:bt.q_start[2], 4:]).all()
+    assert np.isfinite(want[:, :, :4]).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3])
+@pytest.mark.parametrize("T", [2, 9, 60])
+def test_attention_scales_of_16_bits(T, scale):
+    check_attention(R.Batch(94, [100, 5], [T, T], Hq=8, Hkv=2, tree=True), scale=scale)
+
+
+@pytest.mark.parametrize("T", [3, 9, 60])
+def test_attention_layers_of_tiles(T):
+    check_attention(R.Batch(95, [40, 300], [T, T - 1], L=5, Hq=8, Hkv=2, D=128))
+
+
+@pytest.mark.parametrize("T", [3, 9, 60])
+def test_attention_without_tokens(T):
+    """No new tokens at all: nothing is written."""
+    bt = R.Batch(96, [40, 0, 300], [0, 0, 0], Hq=8, Hkv=2, D=128, pad=T)
+    bt.T = T
+    bt.upload()
+    check_attention(bt)
+    same(R.hostf(bt.d["o"]), np.full_like(bt.o, 3.0), "o")
+
+
+@pytest.mark.parametrize("T", [3, 9, 60])
+def test_attention_malformed_starts(T):
+    """Starts that fall, lie outside or span more than T: those sequences are
+    left out, the others are right."""
+    bt = R.Batch(97, [40, 20, 300, 8], [T, 1, 2, 2], Hq=8, Hkv=2, D=128)
+    table, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    for at, to in ((1, T + 9), (1, T + 1), (4, bt.N + 1), (0, -1), (4, bt.q_start[3] - 1)):
+        start = bt.q_start.copy()
+        start[at] = to
+        bt.d["q_start"].copy_(torch.tensor(start))
+        bt.d["o"].fill_(3.0)
+        bt.d["err"].zero_()
+        bt.g_attend()
+        want, tol = R.attend(bt.sh, bt.T, bt.N, start, bt.seq_len, table, None, bt.q,
+                             bt.sh.D ** -0.5, kc, vc, bt.o)
+        close(R.hostf(bt.d["o"]).astype(np.float64), want, tol, "o")
+        assert int(bt.d["err"]) == gb.DEV_ERR_LENGTH
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [3, 30])
+def test_cache_beyond_32_bits(T, dtype):
+    """Pages whose places lie past 2^32 elements and bytes, in both caches."""
+    bt = R.Batch(98, [700, 40, 0], [T, T, T], L=2, Hq=8, Hkv=2, D=256, page=256, dtype=dtype,
+                 tree=True)
+    small, at = bt.sh, 17000  # 256 pages of 256 tokens of 2 heads: 33.5 million elements
+    big = gb.KvShape(small.L, small.B, small.Hq, small.Hkv, small.D, small.page,
+                     at + small.n_pages, small.max_blocks, dtype)
+    d = bt.d
+    caches = {}
+    for n in ("kc", "vc"):
+        caches[n] = torch.empty(getattr(big, {"kc": "k_cache_shape", "vc": "v_cache_shape"}[n]),
+                                dtype=dtype, device="cuda")
+        caches[n][:, at:] = d[n]
+    assert caches["kc"][0].numel() > 2 ** 31 and caches["kc"].numel() > 2 ** 32
+    d.update(caches)
+    table, slots, left, _ = bt.r_reserve()
+    kc, vc, _ = bt.r_append(slots)
+    d["table"].add_(at)
+    d["free"] = torch.cat([d["free"] + at, d["free"].new_full((at,), -1)])
+    bt.sh = big
+    bt.g_reserve()
+    same(R.host(d["slots"]), slots + at * 256, "slots")
+    bt.g_append()
+    bt.g_attend()
+    bt.sh = small
+    want, tol = bt.r_attend(table, kc, vc)
+    close(R.hostf(d["o"]).astype(np.float64), want, tol, "o")
+    keep, path = tree_paths(bt, np.random.default_rng(1))
+    *_, kc, vc, _ = bt.r_commit(keep, path, None, slots, table, bt.free, left, kc, vc)
+    bt.sh = big
+    bt.g_commit(keep, path)
+    same(R.hostf(d["kc"][:, at:]), kc, "k cache")
+    same(R.hostf(d["vc"][:, at:]), vc, "v cache")
+    assert int(d["err"]) == 0
+
+
 def test_attention_same_bits_every_time():
     bt = R.Batch(78, [3000, 40, 700], [9, 300, 1], Hq=8, Hkv=2, D=128)
     check_attention(bt)
