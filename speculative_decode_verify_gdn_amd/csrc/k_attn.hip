@@ -754,7 +754,7 @@ __device__ __forceinline__ void lds_barrier() {
 // N products whose operands read(n) fetches from LDS kAhead products ahead, in this
 // order whatever the compiler would prefer: no product waits for its operand, and
 // no more registers hold operands than that.
-constexpr int kAhead = 4;
+constexpr int kAhead = 8;
 template <int N, typename Read, typename Mul>
 __device__ __forceinline__ void products(Read read, Mul mul) {
   static_assert(N % kAhead == 0, "the ring comes round");
@@ -792,6 +792,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
   __shared__ u32x4 lds0[kBuf], lds1[kBuf];  // keys, then values
   auto buf = [&](int i) { return i == 0 ? lds0 : lds1; };
   __shared__ TreeLds tree;
+  __shared__ int any_odd;
   const KvBatch& k = p.k;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = uni(tid / kWave);
@@ -913,6 +914,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         }
       };
       __syncthreads();  // the last item's LDS is free
+      if (tid == 0) any_odd = 0;
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i)
         if (s0 + i < s1) fetch(s0 + i, buf(i));
@@ -943,7 +945,6 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] = Acc{};
       float m = kNegInf, l = 0.f;
-      bool odd = false;
       auto scores = [&](Acc* sc, const u32x4* kl) {
         const int ka = opaque(k_at);  // the operands' places are worked out anew: few registers
         products<KB * QJ>(
@@ -986,8 +987,13 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
             pf[i][e] = static_cast<__bf16>(w);
           }
       };
-      const auto value_at = [&](int n) {  // operand n of the products with the values
-        return v_at + n / DT * (Mm::kEvery / 8) * D + n % DT * MR;
+      auto values = [&](const bf16x8* pf, const u32x4* vl) {
+        products<NG * DT>(
+            [&](int n) {
+              return __builtin_bit_cast(
+                  bf16x8, vl[v_at + n / DT * (Mm::kEvery / 8) * D + n % DT * MR]);
+            },
+            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
       };
       // A tile that every row sees all of.
       auto plain = [&](const u32x4* kl) {
@@ -997,15 +1003,30 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         bf16x8 pf[NG];
         scores(sc, kl);
         weights(sc, pf);
-        products<NG * DT>(
-            [&](int n) { return __builtin_bit_cast(bf16x8, vl[value_at(n)]); },
-            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
+        values(pf, vl);
       };
       // A tile with keys that some row does not see or that are not there.
       // Values that are not there, infinities and NaN are left out, as in the
-      // stream kernel.
-      auto edge = [&](int kb, uint32_t gone, const u32x4* kl) {
-        const u32x4* const vl = kl + KT * P;
+      // stream kernel: the workgroup puts zeros in their places first.
+      auto edge = [&](int kb, uint32_t gone, u32x4* kl) {
+        u32x4* const vl = kl + KT * P;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int at = i * W * kWave + opaque(tid), first = at / D * 8;
+          const uint32_t there =
+              (gone >> (first / 16)) & 1 ? 0u : chain_sees(len, kb + first, 8);
+          u32x4 w = vl[at] & F::keep(there);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = ((w[e] & F::kExp) + F::kOne) & F::kTop;
+            bad |= y;
+            w[e] &= ~F::spread(y);
+          }
+          vl[at] = w;
+        }
+        if (bad) any_odd = 1;
+        lds_barrier();
         if (kb >= any_sees) return;
         Acc sc[KB];
         bf16x8 pf[NG];
@@ -1028,23 +1049,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
           }
         }
         weights(sc, pf);
-        u32x4 keep[NG];
-#pragma unroll
-        for (int i = 0; i < NG; ++i) keep[i] = F::keep(there_of(i, base_of(i)));
-        uint32_t bad = 0;
-        products<NG * DT>(
-            [&](int n) {
-              u32x4 w = vl[value_at(n)] & keep[n / DT];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t y = ((w[e] & F::kExp) + F::kOne) & F::kTop;
-                bad |= y;
-                w[e] &= ~F::spread(y);
-              }
-              return __builtin_bit_cast(bf16x8, w);
-            },
-            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
-        odd |= bad != 0;
+        values(pf, vl);
       };
 
       // What is in flight when tile s is needed: of NS - 1 tiles, all but the
@@ -1081,7 +1086,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         lds_barrier();
         at = (at + 1) % NS;
       }
-      if (__any(odd)) {  // rare: to the rows that do see them
+      if (any_odd) {  // rare: to the rows that do see them
         const int from = max(s0 * KT, r.ctx & ~(KT - 1)), to = min(len, s1 * KT);
 #pragma unroll 1
         for (int key = from; key < to; ++key) {
