@@ -51,7 +51,8 @@ __device__ __forceinline__ Need kv_need(const KvBatch& k, const KvSpan& r) {
 // by the sequences before its own from the lengths (a few loads per thread: a
 // batch of 256 is one step), so no workgroup waits for another and the call is
 // one launch; the last sequence's workgroup sees the whole batch and writes
-// what is left.  Latency is all there is to it.
+// what is left.  Latency is all there is to it: 5 us of kernel, for 32 sequences of
+// 8 drafts as for 256 of up to 2,048 tokens (a call through the binding takes 13 us).
 constexpr int kChunk = 2048;
 
 __global__ __launch_bounds__(kNT) void k_kv_reserve(KvReserveArgs p) {
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kNT) void k_kv_reserve(KvReserveArgs p) {
     block_scan(taken, lds, total);
     if (tid == 0) *p.n_left = static_cast<int32_t>(n_free - total);
     // rows that belong to no sequence
-    int lo = 0, hi = k.B * k.T;
+    int lo = 0, hi = k.q_start ? 0 : k.B * k.T;
     if (k.q_start) {
       lo = min(max(k.q_start[0], 0), k.N);
       hi = min(max(k.q_start[k.B], lo), k.N);
@@ -141,7 +142,9 @@ __global__ __launch_bounds__(kNT) void k_kv_reserve(KvReserveArgs p) {
 // workgroup takes 64 tokens of one key head.  Keys are copied in 16-byte
 // pieces.  Values change their order: the eight tokens of a channel lie side by
 // side in the cache, so lanes take tokens and each lane writes its 16 bytes of
-// channels one by one.
+// channels one by one: eight lanes complete a piece, and the L2 the lines.  17,000
+// tokens of 4 heads of 128 channels (bf16): 16.4 us, 3.9 TB/s of the 4.8 that a
+// copy reaches; 256 tokens 6 us, which is latency.
 template <typename T, int D>
 __global__ __launch_bounds__(kNT) void k_kv_append(KvAppendArgs p) {
   constexpr int E = 16 / sizeof(T);  // elements of a 16-byte piece
@@ -188,7 +191,9 @@ __global__ __launch_bounds__(kNT) void k_kv_append(KvAppendArgs p) {
 // touch nothing in common.  A wave has several rows of a head on their way at once.
 // A row of k is a few 16-byte pieces, a lane each.  A row of v lies in the cache with
 // 8 slots between two channels, so neighbouring lanes take neighbouring channels
-// and a store touches as few lines as it can.
+// and a store touches as few lines as it can (64 trees over ten layers: 29 us with
+// 16-byte pieces of v, 25 so, 12 with the pages dealt out as below; latency again:
+// 12 MB move, and the path, its slots and its rows are loads that wait for each other).
 template <typename T, int D>
 __device__ void commit_rows(const KvCommitArgs& p, int b, int l) {
   constexpr int E = 16 / sizeof(T);   // elements of a piece

@@ -142,9 +142,9 @@ size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_t
   if (check_kv(shape) != GDN_OK || T < 1 || n_tokens < 1 || n_tokens > kMaxTokens ||
       T > kMaxTokens || !rows_ok(shape, n_tokens))
     return 0;
-  return gdn::attn_workspace(shape->n_layers, shape->batch, T, n_tokens, shape->n_q_heads,
-                             shape->n_kv_heads, shape->head_dim, shape->dtype,
-                             static_cast<long long>(shape->max_blocks) * shape->page_size);
+  return gdn::attn_workspace(
+      static_cast<long long>(T) * (shape->n_q_heads / shape->n_kv_heads), shape->head_dim,
+      shape->dtype);
 }
 
 gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const int32_t* q_start,

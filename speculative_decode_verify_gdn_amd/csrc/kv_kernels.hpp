@@ -121,8 +121,8 @@ hipError_t launch_kv_reserve(const KvReserveArgs& a, hipStream_t s);
 hipError_t launch_kv_append(const KvAppendArgs& a, int head_dim, int dtype, hipStream_t s);
 hipError_t launch_kv_commit(const KvCommitArgs& a, int head_dim, int dtype, hipStream_t s);
 hipError_t launch_attn(const AttnArgs& a, int head_dim, int dtype, hipStream_t s);
-// Bytes of the workspace that launch_attn uses.
-size_t attn_workspace(int L, int B, int T, int N, int Hq, int Hkv, int head_dim, int dtype,
-                      long long max_tokens);
+// Bytes of the workspace that launch_attn uses, for sequences of at most `rows`
+// query rows to a key head.
+size_t attn_workspace(long long rows, int head_dim, int dtype);
 
 }  // namespace gdn
