@@ -532,6 +532,41 @@ def test_commit_writes_every_kept_row(dtype):
     same(R.hostf(bt.d["vc"]), vc, "v cache")
 
 
+def test_commit_gives_back_many_pages():
+    """Sequences that end with thousands of pages beside some of a few and none."""
+    rng = np.random.default_rng(86)
+    ctx = rng.integers(0, 200, 150)
+    ctx[[3, 64, 65, 149]] = [40000, 5000, 1, 17000]
+    bt = R.Batch(86, ctx.tolist(), rng.integers(0, 40, 150).tolist(), Hq=1, Hkv=1)
+    table, slots, left = check_reserve(bt)
+    keep = np.array([rng.integers(0, n + 1) for n in np.diff(bt.q_start)])
+    done = (rng.random(150) < 0.5).astype(np.int64)
+    done[[3, 64, 149]] = 1
+    bt.g_commit(keep, None, done)
+    out, free, top, *_ = bt.r_commit(keep, None, done, slots, table, bt.free, left, bt.kc, bt.vc)
+    same(R.host(bt.d["len_out"]), out, "lengths")
+    same(R.host(bt.d["free"])[:top], free[:top], "stack")
+    assert int(bt.d["n_free"]) == top and int(bt.d["err"]) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_commit_from_slices(dtype):
+    """k and v are slices of one projection's output."""
+    bt = R.Batch(87, [20, 3, 50], [9, 30, 1], L=2, Hq=2, Hkv=2, D=64, dtype=dtype, tree=True)
+    table, slots, left = check_reserve(bt)
+    wide = torch.full((2, bt.N, 3 + 2 + 2, 64), float("nan"), device="cuda", dtype=dtype)
+    wide[:, :, 3:5], wide[:, :, 5:7] = bt.d["k"], bt.d["v"]
+    bt.d["k"], bt.d["v"] = wide[:, :, 3:5], wide[:, :, 5:7]
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    keep, path = tree_paths(bt, np.random.default_rng(2))
+    bt.g_commit(keep, path)
+    *_, kc, vc, err = bt.r_commit(keep, path, None, slots, table, bt.free, left, kc, vc)
+    assert int(bt.d["err"]) == err == 0
+    same(R.hostf(bt.d["kc"]), kc, "k cache")
+    same(R.hostf(bt.d["vc"]), vc, "v cache")
+
+
 def test_commit_errors():
     bt = R.Batch(83, [7, 30, 2, 9], [10, 20, 5, 4])
     path = np.tile(np.arange(20), (4, 1)).astype(np.int64)
