@@ -3,8 +3,8 @@
 //
 // An item is one tile of R query rows (the rows of a key head: G query heads of
 // each token, token by token) against all its keys.  Items are laid on a line,
-// each as long as it costs (its keys, and kItemCost for its start and end), in
-// the order layer, sequence, key head, tile.  Active workgroup w takes the part
+// each as long as it costs (its keys, and as many more as its start and end are
+// worth), in the order layer, sequence, key head, tile.  Active workgroup w takes the part
 // [w, w+1) * total / active of the line, so every workgroup has the same amount
 // of work whatever the lengths are, and at most two items of a workgroup are
 // shared with others: the one that its part begins within (its fragment goes to
@@ -16,8 +16,6 @@
 #include "kv_kernels.hpp"
 
 namespace gdn {
-
-constexpr int kItemCost = 64;  // keys' worth of an item's own work
 
 struct AttnSched {
   long long total;   // length of the line over all layers
@@ -42,12 +40,15 @@ struct AttnItem {
   KvSpan span;
 };
 
-template <int R>
+// ITEM: what an item costs beside its keys, in keys (its queries, the first loads'
+// latency, keys that only some rows see, the outputs or fragments).
+template <int R, int ITEM>
 struct AttnLine {
+  static constexpr int kRows = R;
   // Cost of the first i tiles of one head: a tile costs its cached tokens, the
-  // new ones up to its end at `per` a tile, and kItemCost.
+  // new ones up to its end at `per` a tile, and ITEM.
   static __device__ __forceinline__ long long upto(const KvSpan& r, int per, int i) {
-    return static_cast<long long>(i) * (r.ctx + kItemCost) +
+    return static_cast<long long>(i) * (r.ctx + ITEM) +
            ((static_cast<long long>(i) * (i + 1) * per) >> 1);
   }
   static __device__ __forceinline__ int tiles(const KvSpan& r, int G) {
@@ -105,7 +106,7 @@ struct AttnStart {
   KvSpan span;       // of sequence b
 };
 
-template <int R>
+template <typename Line>
 __device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long long grain) {
   const KvBatch& k = p.k;
   const int lane = threadIdx.x % kWave;
@@ -117,7 +118,7 @@ __device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long
     if (c + lane < k.B) {
       r = kv_span(k, c + lane);
       bad |= !r.ok;
-      v = AttnLine<R>::sequence(r, G, p.Hkv);
+      v = Line::sequence(r, G, p.Hkv);
     }
     upto = wave_scan(v);
   };
@@ -172,15 +173,15 @@ __device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long
 
 // The item at place x of the line, x within the sequence (layer, b) that begins
 // at seq_at.
-template <int R>
+template <typename Line>
 __device__ AttnItem attn_item(const AttnArgs& p, int G, int layer, int b, const KvSpan& span,
                               long long seq_at, long long x) {
   AttnItem it;
   it.layer = layer;
   it.b = b;
   it.span = span;
-  const int nt = AttnLine<R>::tiles(span, G), per = AttnLine<R>::per(G);
-  const long long head = AttnLine<R>::upto(span, per, nt);
+  const int nt = Line::tiles(span, G), per = Line::per(G);
+  const long long head = Line::upto(span, per, nt);
   const long long off = x - seq_at;
   int h = p.Hkv == 1 ? 0
                      : uni(static_cast<int>(static_cast<double>(off) / static_cast<double>(head)));
@@ -191,15 +192,15 @@ __device__ AttnItem attn_item(const AttnArgs& p, int G, int layer, int b, const 
   int lo = 0, hi = nt - 1;  // the last tile that begins at or before `in`
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (AttnLine<R>::upto(span, per, mid) <= in)
+    if (Line::upto(span, per, mid) <= in)
       lo = mid;
     else
       hi = mid - 1;
   }
   it.tile = lo;
-  const long long a = AttnLine<R>::upto(span, per, lo);
+  const long long a = Line::upto(span, per, lo);
   it.at = seq_at + h * head + a;
-  it.cost = AttnLine<R>::upto(span, per, lo + 1) - a;
+  it.cost = Line::upto(span, per, lo + 1) - a;
   return it;
 }
 

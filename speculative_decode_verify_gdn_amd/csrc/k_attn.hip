@@ -245,6 +245,9 @@ struct Stream {
   static constexpr int kStep = 32 * W;   // keys of one step of the workgroup
   static constexpr int QLD = D + Frag<T>::kPad;
   static constexpr int kC = D < 128 ? D : 128;  // channels joined at a time
+  // (24 long contexts in bf16: 89 us with 64, 86 with 128; 16 in 32 bits, whose keys
+  // take longer: 27.4 and 28.5)
+  typedef AttnLine<R, sizeof(T) == 2 ? 128 : 64> Line;
   struct Lds {
     union {  // one after the other
       T q[R * QLD];
@@ -259,6 +262,7 @@ struct Stream {
 template <typename T, int D, int NT>
 __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, long long grain) {
   using St = Stream<T, D, NT>;
+  using Line = typename St::Line;
   using F = Frag<T>;
   constexpr int W = St::W, R = St::R, QLD = St::QLD;
   constexpr int KJ = D / F::kPerK;  // score products per tile
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
   const float inv_g = 1.f / static_cast<float>(G);
   const int wg = blockIdx.x;
   const Places<R, D> places(p.ws, n_wg);
-  const AttnStart st = attn_start<R>(p, G, wg, n_wg, grain);
+  const AttnStart st = attn_start<Line>(p, G, wg, n_wg, grain);
   AttnJoin join;
   join.last = -1;
   // scores are compared unscaled (a negative scale turns q's sign); at least
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
   int layer = st.layer, b = st.b;
   KvSpan r = st.span;
   while (x < st.hi) {
-    const AttnItem it = attn_item<R>(p, G, layer, b, r, seq_at, x);
+    const AttnItem it = attn_item<Line>(p, G, layer, b, r, seq_at, x);
     const long long end = it.at + it.cost;
     const long long till = end < st.hi ? end : st.hi;
     const int row0 = it.tile * R;
@@ -623,7 +627,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
     }
     x = till;
     if (x < st.hi) {  // the next item, of this sequence or of the next that has any
-      long long seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+      long long seq_end = seq_at + Line::sequence(r, G, p.Hkv);
       while (x >= seq_end) {
         seq_at = seq_end;
         if (++b == k.B) {
@@ -631,7 +635,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
           ++layer;
         }
         r = kv_span(k, b);
-        seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+        seq_end = seq_at + Line::sequence(r, G, p.Hkv);
       }
     }
   }
@@ -747,6 +751,8 @@ struct Tile {
   static constexpr int kPieces = D / 8;                         // 16-byte pieces of a key
   static constexpr int kLoads = kKeys * kPieces / (W * kWave);  // of a wave, K and V each
   static constexpr int kKeysPerLoad = W * kWave / kPieces;      // of the workgroup
+  // (64 keys' worth for all: prompts 634 us, trees 219, drafts 63; so 605, 202, 61)
+  typedef AttnLine<ROWS, ROWS == 64 ? 256 : 448> Line;
 };
 
 // 16 bytes per lane, from a uniform address and the lane's own offset in bytes to
@@ -796,6 +802,7 @@ template <int D, int ROWS>
 __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(AttnArgs p, int n_wg,
                                                                            long long grain) {
   using Tl = Tile<D, ROWS>;
+  using Line = typename Tl::Line;
   using Mm = typename Tl::Mma;
   typedef typename Mm::Acc Acc;
   using F = Frag<uint16_t>;
@@ -821,7 +828,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
                            static_cast<int>(blockIdx.x) / kNumXcd
                      : static_cast<int>(blockIdx.x);
   const Places<R, D> places(p.ws, n_wg);
-  const AttnStart st = attn_start<R>(p, G, wg, n_wg, grain);
+  const AttnStart st = attn_start<Line>(p, G, wg, n_wg, grain);
   AttnJoin join;
   join.last = -1;
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
@@ -848,7 +855,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
   int layer = st.layer, b = st.b;
   KvSpan r = st.span;
   while (x < st.hi) {
-    const AttnItem it = attn_item<R>(p, G, layer, b, r, seq_at, x);
+    const AttnItem it = attn_item<Line>(p, G, layer, b, r, seq_at, x);
     const long long end = it.at + it.cost;
     const long long till = end < st.hi ? end : st.hi;
     const int row0 = it.tile * R;
@@ -1166,7 +1173,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
     }
     x = till;
     if (x < st.hi) {  // the next item, of this sequence or of the next that has any
-      long long seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+      long long seq_end = seq_at + Line::sequence(r, G, p.Hkv);
       while (x >= seq_end) {
         seq_at = seq_end;
         if (++b == k.B) {
@@ -1174,7 +1181,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
           ++layer;
         }
         r = kv_span(k, b);
-        seq_end = seq_at + AttnLine<R>::sequence(r, G, p.Hkv);
+        seq_end = seq_at + Line::sequence(r, G, p.Hkv);
       }
     }
   }
@@ -1387,6 +1394,8 @@ AttnPlan attn_plan(long long rows, int head_dim, int size) {
     AttnPlan a{0, 1, 2 * kCus};
   if (size == 2 && rows > 16) {
     a.tile = rows > 64 ? 128 : 64;
+    // LDS for one workgroup on a CU (64 trees: 186 us; two parts for each 202)
+    if (a.tile == 128 && head_dim == 256) a.wgs = kCus;
     return a;
   }
   const int most = stream_most(head_dim, size);
