@@ -247,10 +247,13 @@ def _run_own(s):
         if op == "attend":
             s["workspace"] = torch.empty(gb.attn_verify_workspace_bytes(s["shape"], s["T"], s["N"]),
                                          dtype=torch.uint8, device="cuda")
+            if s["parent"] is not None:  # one entry for each of the N rows, of no sequence too
+                behind = s["N"] - s["parent"].shape[0]
+                s["parents"] = torch.cat([s["parent"], s["parent"].new_full((behind,), -1)])
     sh = s["shape"]
     if op == "attend":
         gb.attn_verify(sh, s["q"], s["seq_len"], s["table"], s["k_cache"], s["v_cache"], s["o"],
-                       s["workspace"], s["T"], q_start=s["q_start"], parent=s["parent"],
+                       s["workspace"], s["T"], q_start=s["q_start"], parent=s.get("parents"),
                        dev_err=s["dev_err"])
         return s["o"]
     if op == "reserve":
