@@ -663,9 +663,9 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 // itself: 289 against 235 us for 64 trees of 64 nodes, 16 query heads).
 //
 // Three prompts of about 3,000 tokens behind 1,000 cached ones, 32 query heads of
-// 128 channels: 630 us, 855 TFLOP/s; a large matrix product reaches 1,189.  The
+// 128 channels: 600 us, 900 TFLOP/s; a large matrix product reaches 1,189.  The
 // rest is the vector work of the softmax, which the matrix pipe hides in part.
-// 64-row tiles of 32 drafted chunks: 53 us, 3.7 TB/s, between the two bounds.
+// 64-row tiles of 32 drafted chunks: 52 us, 3.8 TB/s, between the two bounds.
 //
 // LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
 // rows that are read together fall on different banks; values as in the cache,
@@ -1370,9 +1370,13 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   }
 }
 
-// A workgroup has at least this many keys (in 32 bits, where a key's products take
-// sixteen times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64).
+// A workgroup has at least this many keys' cost.  Stream kernel in bf16 256 (one
+// sequence of 800 tokens: level with 128); in 32 bits, where a key's products take
+// sixteen times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64.
+// Tile kernel: one tree of 64 nodes behind 2,000 tokens 38 us with 256, 35 with 128,
+// 34.5 with 96; two prompts of 1,000 tokens and 6 heads 44, 42.5 and 42.8.
 constexpr long long grain_of(int size) { return size == 2 ? 256 : 64; }
+constexpr long long kTileGrain = 128;
 constexpr int kCus = 256;
 static_assert(2 * kCus <= kMostWg, "the join counts no more");
 
@@ -1423,7 +1427,7 @@ hipError_t stream_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 template <int D, int ROWS>
 hipError_t tile_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  k_attn_tile<D, ROWS><<<p.wgs, Tile<D, ROWS>::W * kWave, 0, s>>>(a, p.wgs, grain_of(2));
+  k_attn_tile<D, ROWS><<<p.wgs, Tile<D, ROWS>::W * kWave, 0, s>>>(a, p.wgs, kTileGrain);
   return join_t<uint16_t, D, ROWS>(a, p.wgs, s);
 }
 
