@@ -439,8 +439,8 @@ gdn_status kv_reserve(const kv_shape* shape, int32_t T, int32_t n_tokens, const 
 /*
  * Write L layers' new keys and values into their slots.
  *   k, v  [L,n_tokens,Hkv,D] with k_ld (v_ld) elements from one token to the
- *         next (>= Hkv*D and a multiple of 16 bytes; a layer takes n_tokens *
- *         ld), so they may be slices of one projection's output
+ *         next (>= Hkv*D, at most 2^20, and a multiple of 16 bytes; a layer
+ *         takes n_tokens * ld), so they may be slices of one projection's output
  *   slots [n_tokens] int32 as kv_reserve gives them; -1 skips the token.  Any
  *         other slot outside the pool skips it and sets GDN_DEV_ERR_PAGE.  Two
  *         tokens of a call may not share a slot.

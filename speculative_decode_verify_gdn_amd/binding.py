@@ -191,8 +191,15 @@ def _check(status: int, what: str):
         raise GdnError(status, what)
 
 
+# The current stream's handle without a Stream object around it, which takes 3 us
+# of a small call's 12.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

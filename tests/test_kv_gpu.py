@@ -672,6 +672,25 @@ def test_rounds_together(tree, graph):
     run_rounds(7, tree, 90 + tree, graph=graph)
 
 
+def test_calls_follow_the_current_stream():
+    """Without a stream argument a call goes to the current one: here behind work
+    that gives it its inputs."""
+    bt, want = (R.Batch(93, [2000, 5], [3, 20], Hq=8, Hkv=2, D=128) for _ in range(2))
+    want.g_reserve(), want.g_append(), want.g_attend()
+    q = bt.d["q"].clone()
+    bt.d["q"].zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        x = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            x = x @ x * 1e-3
+        bt.d["q"].copy_(q)
+        bt.g_reserve(), bt.g_append(), bt.g_attend()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(bt.d["o"], want.d["o"])
+
+
 def test_two_streams_at_once():
     """Two batches on two streams with no wait between them end where they end
     alone."""
