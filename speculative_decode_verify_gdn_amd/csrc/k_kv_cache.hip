@@ -52,7 +52,7 @@ __device__ __forceinline__ Need kv_need(const KvBatch& k, const KvSpan& r) {
 // batch of 256 is one step), so no workgroup waits for another and the call is
 // one launch; the last sequence's workgroup sees the whole batch and writes
 // what is left.  Latency is all there is to it: 5 us of kernel, for 32 sequences of
-// 8 drafts as for 256 of up to 2,048 tokens (a call through the binding takes 13 us).
+// 8 drafts as for 256 of up to 2,048 tokens (a call through the binding takes 10 us).
 constexpr int kChunk = 2048;
 
 __global__ __launch_bounds__(kNT) void k_kv_reserve(KvReserveArgs p) {
