@@ -384,8 +384,8 @@ gdn_status gdn_conv_state_rollback(const gdn_shape* shape, int32_t T, void* conv
  * Sequences are either uniform, T new tokens each ([B,T,...], q_start NULL,
  * n_tokens >= B*T), or packed: sequence b's new tokens are rows q_start[b] ..
  * q_start[b+1]-1 of n_tokens, at most T of them and possibly none.  Rows
- * behind the last sequence are never read or written (kv_reserve gives them
- * slot -1).
+ * of no sequence (behind the last, before the first, of one that is left out)
+ * are never read or written; kv_reserve gives them slot -1.
  *
  * Caches (dtype as k and v), per layer:
  *   k_cache [L,P,Hkv,page,Dk]       a token's key in one piece
@@ -400,7 +400,9 @@ gdn_status gdn_conv_state_rollback(const gdn_shape* shape, int32_t T, void* conv
  * attn_verify n_tokens * n_q_heads / n_kv_heads <= 2^30.  A sequence whose
  * lengths are malformed (q_start decreasing or outside [0, n_tokens], more than
  * T new tokens, seq_len < 0, seq_len + new > max_blocks * page_size) sets
- * GDN_DEV_ERR_LENGTH and is left out.
+ * GDN_DEV_ERR_LENGTH and is left out.  Where starts fall, two sequences that
+ * are well-formed each for itself may claim the same row; what such a row
+ * gets is one of the two's.
  */
 typedef struct {
   int32_t n_layers;   /* L: leading dimension of every per-layer tensor */
@@ -424,7 +426,8 @@ typedef struct {
  *   n_free      [1] int32: pages free before;  n_left [1]: after.  They may
  *               not be the same address; free_pages is not written, so until
  *               kv_commit the same call gives the same answer
- *   slots       [n_tokens] int32: the slot of every new token
+ *   slots       [n_tokens] int32: the slot of every new token, and -1 in every
+ *               row that no served sequence owns: all of it is written
  * Pages are taken from the top of the stack in order of sequence, then of
  * block.  A sequence is served while its pages and those of all sequences
  * before it fit in n_free (one that needs none always is); the others get slot

@@ -709,3 +709,48 @@ def test_two_streams_at_once():
     for a, b in zip(alone, both):
         for n in ("slots", "table", "kc", "vc", "o", "n_left"):
             assert torch.equal(a.d[n], b.d[n]), n
+
+
+# ---- rows of no sequence
+
+STARTS = [  # of sequences of 3, 4, 5 and 2 tokens, T = 5, 18 rows: which start, and its value
+    {2: 12}, {3: 14}, {2: 1}, {0: -1}, {0: 2}, {0: 17}, {4: 19}, {4: 11}, {4: 3}, {4: -1},
+    {1: 1 << 30}, {1: -(1 << 31)}, {0: 5, 1: 4, 2: 3, 3: 2, 4: 1}, {0: 18, 1: 0, 2: 18, 3: 0, 4: 18}]
+
+
+@pytest.mark.parametrize("at", STARTS, ids=str)
+def test_reserve_clears_rows_of_no_sequence(at):
+    """Whatever the starts, every row that no served sequence owns gets slot -1,
+    and no other row does: kv_append runs on the same array and writes where it says."""
+    bt = R.Batch(101, [5, 30, 2, 40], [3, 4, 5, 2], Hkv=1, Hq=1, pad=4)
+    for i, v in at.items():
+        bt.q_start[i] = v
+    bt.upload()
+    bt.d["slots"].copy_(torch.arange(bt.N) * 3 % (bt.sh.n_pages * 16))  # an earlier round's
+    _, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    same(R.hostf(bt.d["kc"]), kc, "k cache")
+    same(R.hostf(bt.d["vc"]), vc, "v cache")
+
+
+@pytest.mark.parametrize("T", [4, 39])
+@pytest.mark.parametrize("B", [3, 256, 700])
+def test_reserve_clears_rows_of_sequences_too_long(B, T):
+    rng = np.random.default_rng(B)
+    bt = R.Batch(102, rng.integers(0, 100, B).tolist(), rng.integers(0, 40, B).tolist(), pad=5)
+    bt.T = T
+    bt.seq_len[B // 2] = -1
+    bt.upload()
+    bt.d["slots"].fill_(16)
+    check_reserve(bt)
+
+
+def test_reserve_clears_many_rows():
+    """More rows than are looked at in one go, of a sequence too long between two
+    that are served."""
+    bt = R.Batch(103, [3, 900, 70], [70000, 75000, 60000], Hkv=1, Hq=1, page=256, pad=70000)
+    bt.T = 70000
+    bt.upload()
+    bt.d["slots"].fill_(16)
+    check_reserve(bt)
