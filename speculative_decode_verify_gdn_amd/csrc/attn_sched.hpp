@@ -37,14 +37,12 @@ struct AttnJoin {
 struct AttnItem {
   int layer, b, h, tile;
   long long at, cost;  // start on the line, length
-  KvSpan span;
 };
 
 // ITEM: what an item costs beside its keys, in keys (its queries, the first loads'
 // latency, keys that only some rows see, the outputs or fragments).
 template <int R, int ITEM>
 struct AttnLine {
-  static constexpr int kRows = R;
   // Cost of the first i tiles of one head: a tile costs its cached tokens, the
   // new ones up to its end at `per` a tile, and ITEM.
   static __device__ __forceinline__ long long upto(const KvSpan& r, int per, int i) {
@@ -179,7 +177,6 @@ __device__ AttnItem attn_item(const AttnArgs& p, int G, int layer, int b, const 
   AttnItem it;
   it.layer = layer;
   it.b = b;
-  it.span = span;
   const int nt = Line::tiles(span, G), per = Line::per(G);
   const long long head = Line::upto(span, per, nt);
   const long long off = x - seq_at;

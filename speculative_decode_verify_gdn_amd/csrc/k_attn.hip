@@ -24,7 +24,6 @@
 // probability is rounded once, as an operand (2^-8 of itself, as the output is
 // again), and the sum l takes it before that.
 
-#include <algorithm>
 #include <type_traits>
 
 #include "attn_sched.hpp"
@@ -39,8 +38,6 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr float kSlack = 8.f;
 
 // ---- element types: 32 keys of K and V as MFMA operands
-
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 template <typename T>
 struct Frag;

@@ -8,8 +8,6 @@
 // found by a prefix sum over the batch.  No atomics take part in that, so the
 // same inputs give the same pages every time.
 
-#include <algorithm>
-
 #include "gdn_common.hpp"
 #include "kv_kernels.hpp"
 
@@ -92,7 +90,7 @@ __device__ void clear_rows_of_none(const KvBatch& k, int32_t* slots, bool odd) {
 
 __global__ __launch_bounds__(kNT) void k_kv_reserve(KvReserveArgs p) {
   __shared__ long long lds[kNT / kWave];
-  __shared__ long long sh_before, sh_taken;
+  __shared__ long long sh_before;
   const KvBatch& k = p.k;
   const int b = blockIdx.x, tid = threadIdx.x;
   const KvSpan me = kv_span(k, b);
