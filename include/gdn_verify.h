@@ -507,9 +507,10 @@ size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_t
  * n_keep outside [0, new tokens] sets GDN_DEV_ERR_N_KEEP and a path entry
  * outside them GDN_DEV_ERR_PATH; of such a sequence nothing is kept.  Nothing
  * is kept of a sequence that kv_reserve did not serve (first slot -1); n_keep > 0
- * then sets GDN_DEV_ERR_NO_PAGES.  It has no new pages to give back, and its old
- * ones go only with done.  With path NULL, k, v
- * and the caches are not used and may be NULL.
+ * then sets GDN_DEV_ERR_NO_PAGES.  No new pages of it are given back (it has
+ * none, unless its first slot is -1 for a page number outside the pool: then
+ * the others taken for it stay out of the pool), and its old ones go only with
+ * done.  With path NULL, k, v and the caches are not used and may be NULL.
  * Source: GDN page s4 (the window rebuilt from the accepted raw tokens), for
  * the attention layers' cache.
  */

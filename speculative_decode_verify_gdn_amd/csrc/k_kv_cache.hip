@@ -236,6 +236,7 @@ __device__ void commit_rows(const KvCommitArgs& p, int b, int l) {
   int node = lane < n ? p.path[static_cast<size_t>(b) * k.T + lane] : 0;
   int slot = lane < n ? p.slots[r.s + lane] : -1;
   if (__any(node < 0 || node >= r.n)) return;
+  if (__shfl(slot, 0, kWave) < 0) return;  // not served: commit_counts keeps nothing of it
   if (slot >= k.n_pages << k.page_shift) slot = -1;
   const int ps = 1 << k.page_shift;
   const size_t head = static_cast<size_t>(ps) * D;

@@ -586,6 +586,18 @@ def test_commit_of_sequences_that_were_not_served():
     check_commit(bt, np.array([3, 0, 1, 0]), None, np.array([0, 0, 0, 1]), err=R.NO_PAGES)
 
 
+def test_commit_keeps_nothing_behind_a_first_slot_of_none():
+    """A bad page number under the first new token, good ones under the next: the
+    counts keep nothing, and so do the caches."""
+    bt = R.Batch(106, [13, 30], [9, 12], L=2, Hq=2, Hkv=2)
+    bt.table[0, 0] = bt.sh.n_pages
+    bt.upload()
+    slots = bt.r_reserve()[1]
+    assert (slots[:9] >= 0).tolist() == [False] * 3 + [True] * 6
+    path = np.stack([np.arange(11, -1, -1) % 9, np.arange(12)]).astype(np.int64)
+    check_commit(bt, np.array([8, 5]), path, None, err=R.NO_PAGES)
+
+
 # ---- together, as a round makes them
 
 def run_rounds(rounds, tree, seed, stream=None, graph=False):
