@@ -474,8 +474,11 @@ gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int
  * with bf16 the probabilities are rounded to bf16 for the product with V.
  * Cache places behind a sequence's last token may hold anything, NaN included.
  * So may masked new tokens: an infinite or NaN value (or key) of a token
- * reaches only the rows that attend to it.  A score of -inf counts for nothing;
- * a row all of whose scores are such is 0.  A malformed parent array sets
+ * reaches only the rows that attend to it.  It reaches all of those, however
+ * small its weight: the value's channel is then infinite or NaN (which of them,
+ * IEEE arithmetic decides: a weight that is 0 in fp32, as a score of -inf has it,
+ * makes 0 * inf).  Otherwise a score of -inf counts for nothing; a row all of
+ * whose scores are such is 0, whatever the values are.  A malformed parent array sets
  * GDN_DEV_ERR_PARENT and leaves the sequence's rows of o unwritten.  A page
  * number outside the pool sets GDN_DEV_ERR_PAGE; its tokens then count as
  * masked, and the rows of that sequence are meaningless.  The result is the same

@@ -6,7 +6,9 @@
 // in one pass over the keys with the running maximum m, sum l and output O of
 // each row: a step with scores s rescales l and O by exp(m - m') and adds
 // exp(s - m') (times v).  Two such triples over disjoint keys join the same way
-// (the waves of a workgroup, then the fragments of an item).
+// (the waves of a workgroup, then the fragments of an item).  No triple is left out of
+// a sum, whatever its weight: an infinity in its O must reach the row (0 * inf is NaN).
+// Only a row whose whole l is 0, all its scores -inf, is written as 0.
 //
 // Everything is computed transposed, S^T = K Q^T and O^T = V^T P^T, so that a
 // lane owns one query row: its column of a 16x16 result tile.  Maximum, sum
@@ -565,7 +567,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
           for (int t = 0; t < St::kC / 16; ++t) {
             floatx4 v = o[n][ch * (St::kC / 16) + t];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = mine[n] == 0.f ? 0.f : v[i] * mine[n];
+            for (int i = 0; i < 4; ++i) v[i] *= mine[n];
             *reinterpret_cast<floatx4*>(&sh.join[wave][n * 16 + c][t * 16 + 4 * g]) = v;
           }
         __syncthreads();
@@ -608,7 +610,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
                      (static_cast<long long>(tok) * p.Hq + skip + rr - tok * G) * D + dd;
             T e4[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) e4[j] = to_out(v[j] * inv, T{});
+            for (int j = 0; j < 4; ++j) e4[j] = to_out(inv == 0.f ? 0.f : v[j] * inv, T{});
             __builtin_memcpy(__builtin_assume_aligned(dst, 4 * sizeof(T)), e4, sizeof(e4));
           } else {
             *reinterpret_cast<floatx4*>(places.row(place, rr) + dd) = v;
@@ -1142,7 +1144,8 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
             for (int a = 0; a < Mm::kAcc / 4; ++a) {
               uint16_t e4[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e4[i] = to_out(o[t][4 * a + i] * inv, uint16_t{});
+              for (int i = 0; i < 4; ++i)
+                e4[i] = to_out(l == 0.f ? 0.f : o[t][4 * a + i] * inv, uint16_t{});
               __builtin_memcpy(__builtin_assume_aligned(dst + t * MR + 8 * a, 8), e4, 8);
             }
         } else {
@@ -1200,15 +1203,14 @@ struct Partial {
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = 0.f;
   }
+  // A sum that has seen no key but those of score -inf has no weight.
   __device__ __forceinline__ void add(const Partial& y, float c2) {
-    if (y.m == kNegInf && y.l == 0.f) return;  // no keys
     const float M = fmaxf(m, y.m);
     const float a = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - M) * c2);
-    const float b = __builtin_amdgcn_exp2f((y.m - M) * c2);
-    // a sum of no weight is left out: it may be an infinity
-    l = (a == 0.f && l == l ? 0.f : l * a) + y.l * b;
+    const float b = y.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((y.m - M) * c2);
+    l = l * a + y.l * b;
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = (a == 0.f ? 0.f : o[i] * a) + (b == 0.f ? 0.f : y.o[i] * b);
+    for (int i = 0; i < E; ++i) o[i] = o[i] * a + y.o[i] * b;
     m = M;
   }
 };
@@ -1225,6 +1227,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   const Places<R, D> places(p.ws, n_wg);
   constexpr int E = D / kWave;
   __shared__ float weight[RB][kMostWg];  // of a fragment, over l of them all
+  __shared__ float all[RB];              // that l
   __shared__ float part[3][RB][D];
   __shared__ int upto[kMostWg];  // tasks of the items that workgroups 0 .. w began
   __shared__ int wave_sum_[2][4];
@@ -1287,7 +1290,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
       const float inv = y.l == 0.f ? 0.f : 1.f / y.l;
       T e[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) e[i] = to_out(y.o[i] * inv, T{});
+      for (int i = 0; i < E; ++i) e[i] = to_out(y.l == 0.f ? 0.f : y.o[i] * inv, T{});
       __builtin_memcpy(__builtin_assume_aligned(out, E * sizeof(T)), e, sizeof(e));
     };
     if (few) {
@@ -1325,6 +1328,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
         weight[i][f] = w;
       }
       L = wave_sum(L);
+      if (lane == 0) all[i] = L;
       const float inv = L == 0.f ? 0.f : 1.f / L;
       for (int f = lane; f < n; f += kWave) weight[i][f] *= inv;
     }
@@ -1336,12 +1340,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
       for (int i = 0; i < RB; ++i) {
         const float* from = places.row(place(f), min(row0 + i, j.rows - 1));
         const float w = weight[i][f];
-        // a sum of no weight is left out: it may be an infinity, or never written
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float v = from[lane * E + e];
-          o[i][e] += w == 0.f ? 0.f : v * w;
-        }
+        for (int e = 0; e < E; ++e) o[i][e] += from[lane * E + e] * w;
       }
     if (wave > 0)
 #pragma unroll
@@ -1354,7 +1354,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
       for (int i = 0; i < RB; ++i) {
         if (row0 + i >= j.rows) continue;
         Partial<E> y;
-        y.l = 1.f;
+        y.l = all[i] == 0.f ? 0.f : 1.f;  // the weights are over it already
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           y.o[e] = o[i][e];

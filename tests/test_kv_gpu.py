@@ -364,6 +364,63 @@ def test_attention_keys_whose_scores_are_infinite(T, dtype):
     assert np.isfinite(want[:, :, :4]).all()
 
 
+def check_not_finite(bt, zero):
+    """Rows of `zero` [N,Hq], all of whose scores are minus infinity, are 0; elsewhere
+    what is finite in the plain form is right and what is not is not."""
+    table, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    bt.g_attend()
+    with np.errstate(all="ignore"):
+        want, tol = bt.r_attend(table, kc, vc)
+    got = R.hostf(bt.d["o"]).astype(np.float64)
+    assert (got[:, zero] == 0).all()
+    assert np.isnan(want[:, zero]).all()
+    got, want, tol = got[:, ~zero], want[:, ~zero], tol[:, ~zero]
+    fin = np.isfinite(want)
+    assert (np.isfinite(got) == fin).all()
+    close(got[fin], want[fin], tol[fin], "o")
+    assert fin.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx", [0, 70, 700, 5000])
+@pytest.mark.parametrize("Hq,T", [(4, 3), (16, 3), (16, 9)])
+def test_attention_values_beside_scores_of_minus_infinity(Hq, T, ctx, dtype):
+    """The first sequence's cached keys and first two new ones score minus infinity
+    for head 0, and some of their values are not finite.  Its first two rows are 0
+    there; the others see a key that counts."""
+    bt = R.Batch(104, [ctx, 33], [T, T], Hq=Hq, Hkv=2, D=64, dtype=dtype)
+    bt.q[..., 3] = np.abs(bt.q[..., 3]) + 0.5
+    for j in range(ctx):
+        bt.kc[:, bt.table[0, j // 16], 0, j % 16, 3] = -np.inf
+    for j, to in ((40, np.inf), (ctx - 1, -np.inf), (ctx // 2, np.nan)):
+        if 0 <= j < ctx:
+            bt.vc[:, bt.table[0, j // 16], 0, j % 16 // 8, 5 + j % 3, j % 8] = to
+    bt.k[:, :2, 0, 3] = -np.inf
+    bt.v[:, 0, 0, 9], bt.v[:, 1, 0, 10] = np.inf, np.nan
+    bt.upload()
+    zero = np.zeros((bt.N, Hq), bool)
+    zero[:2, :Hq // 2] = True
+    check_not_finite(bt, zero)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx", [700, 5000])
+@pytest.mark.parametrize("Hq,T", [(4, 3), (16, 3), (16, 9)])
+def test_attention_infinite_values_of_little_weight(Hq, T, ctx, dtype):
+    """An infinite value reaches its rows however small its weight, wherever its
+    key lies: among the first keys, whose scores are hundreds below the others'."""
+    bt = R.Batch(105, [ctx, 33], [T, T], Hq=Hq, Hkv=2, D=64, dtype=dtype)
+    bt.q[..., 3] = np.abs(bt.q[..., 3]) + 0.5
+    for j in range(ctx // 2):
+        bt.kc[:, bt.table[0, j // 16], 0, j % 16, 3] = -8000.0
+    for j, to in ((3, np.inf), (40, -np.inf), (ctx // 2 - 1, np.nan)):
+        bt.vc[:, bt.table[0, j // 16], 0, j % 16 // 8, 20 + j % 8, j % 8] = to
+    bt.upload()
+    check_not_finite(bt, np.zeros((bt.N, Hq), bool))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3])
 @pytest.mark.parametrize("T", [2, 9, 60])
 def test_attention_scales_of_16_bits(T, scale):
