@@ -790,11 +790,9 @@ __device__ __forceinline__ void products(Read read, Mul mul) {
     __builtin_amdgcn_sched_barrier(0);
   }
 }
-// Until all but the last N of the wave's loads into LDS have arrived (vmcnt N).
-template <int N>
+// Until the wave's loads into LDS have arrived.
 __device__ __forceinline__ void lds_loads_done() {
-  static_assert(N < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0
 }
 
 template <int D, int ROWS>
@@ -810,7 +808,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
   constexpr int MR = Mm::kRows, PT = kWave / MR;  // rows of a wave, lanes of a row
   // separate objects, so that the compiler sees that loads into one buffer do
   // not touch what is read from the other
-  constexpr int NS = 2, kBuf = 2 * KT * P;
+  constexpr int kBuf = 2 * KT * P;
   __shared__ u32x4 lds0[kBuf], lds1[kBuf];  // keys, then values
   auto buf = [&](int i) { return i == 0 ? lds0 : lds1; };
   __shared__ TreeLds tree;
@@ -910,9 +908,9 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
       const char* kw = reinterpret_cast<const char*>(kc + wave * kWave / P % 16 * D);
       const char* vw =
           reinterpret_cast<const char*>(vc + (wave * kWave / D % 2 * D + wave * kWave % D) * 8);
-      uint32_t gones = 0;
-      // Sixteens without a page, of all tiles in flight; a tile's are looked at
-      // when it is multiplied (only then does a page number that is not one count).
+      // Sixteens without a page of the tile last sent, looked at when it is multiplied
+      // (only then does a page number that is not one count).
+      uint32_t gone_sent = 0;
       // Sends the tile of step s on its way into the buffers: load j of a wave
       // fills 64 pieces in a row, of keys (and of values: eight keys of a channel
       // to a piece) that lie in one sixteen.
@@ -920,8 +918,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         u32x4* const vl = kl + KT * P;
         const int at = s * (KT / 16);
         if (at - batch == 64) enter(at, pgn);
-        gones = gones << (KT / 16) |
-                (static_cast<uint32_t>(gone_all >> (at - batch)) & ((1u << (KT / 16)) - 1u));
+        gone_sent = static_cast<uint32_t>(gone_all >> (at - batch)) & ((1u << (KT / 16)) - 1u);
         const int six0 = at - batch + wave * kWave / P / 16;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -937,9 +934,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
       };
       __syncthreads();  // the last item's LDS is free
       if (tid == 0) any_odd = 0;
-#pragma unroll
-      for (int i = 0; i < NS - 1; ++i)
-        if (s0 + i < s1) fetch(s0 + i, buf(i));
+      if (s0 < s1) fetch(s0, buf(0));
       // the lane's row
       const int myrow = min(wave * MR + c, rows - 1);
       const int tok = tile_token(skip, myrow, inv_g);
@@ -1074,39 +1069,28 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         values(pf, vl);
       };
 
-      // What is in flight when tile s is needed: of NS - 1 tiles, all but the
-      // oldest may stay so, unless no more are being sent.
-      lds_loads_done<0>();
+      lds_loads_done();
       lds_barrier();
-      int s = s0, at = 0;  // at = (s - s0) % NS
-      auto is_gone = [&](int step) {  // of tile `step`, the oldest in flight
-        const int newer = min(step + NS - 2, s1 - 1) - step;
-        return gones >> (newer * (KT / 16)) & ((1u << (KT / 16)) - 1u);
-      };
-      while (s < s1 && (s + 1) * KT <= all_see && is_gone(s) == 0) {
+      int s = s0, at = 0;  // at: the buffer of tile s
+      while (s < s1 && (s + 1) * KT <= all_see && gone_sent == 0) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const bool more = s + NS - 1 < s1;
-          if (more) fetch(s + NS - 1, buf((i + NS - 1) % NS));
+        for (int i = 0; i < 2; ++i) {
+          if (s + 1 < s1) fetch(s + 1, buf(1 - i));
           plain(buf(i));
-          if (more)
-            lds_loads_done<(NS - 2) * 2 * NL>();
-          else
-            lds_loads_done<0>();
+          lds_loads_done();
           lds_barrier();
           ++s;
-          at = (i + 1) % NS;
-          if (!(s < s1 && (s + 1) * KT <= all_see && is_gone(s) == 0)) break;
+          at = 1 - i;
+          if (!(s < s1 && (s + 1) * KT <= all_see && gone_sent == 0)) break;
         }
       }
       for (; s < s1; ++s) {
-        const uint32_t gone = is_gone(s);
-        const int to = (at + NS - 1) % NS;
-        if (s + NS - 1 < s1) fetch(s + NS - 1, buf(to));
+        const uint32_t gone = gone_sent;
+        if (s + 1 < s1) fetch(s + 1, buf(1 - at));
         edge(s * KT, gone, buf(at));
-        lds_loads_done<0>();
+        lds_loads_done();
         lds_barrier();
-        at = (at + 1) % NS;
+        at = 1 - at;
       }
       if (any_odd) {  // rare: to the rows that do see them
         const int from = max(s0 * KT, r.ctx & ~(KT - 1)), to = min(len, s1 * KT);
