@@ -12,6 +12,7 @@
 // k_attn_join adds the fragments of a shared item in order of w.
 #pragma once
 
+#include "attn_parts.hpp"
 #include "gdn_common.hpp"
 #include "kv_kernels.hpp"
 
@@ -98,14 +99,16 @@ __device__ __forceinline__ long long wave_scan(long long v) {
 // a call of few keys waits for is this chain of latencies).  Uniform.
 struct AttnStart {
   AttnSched s;
-  long long lo, hi;  // this workgroup's part; empty if it has none
+  int wg;            // this workgroup's number on the line
+  long long lo, hi;  // its part; empty if it has none
   int layer, b;      // of the first item
   long long seq_at;  // where sequence b begins
   KvSpan span;       // of sequence b
 };
 
-template <typename Line>
-__device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long long grain) {
+// NEAR: neighbours on the line to one XCD.
+template <typename Line, bool NEAR>
+__device__ AttnStart attn_start(const AttnArgs& p, int G, int n_wg, long long grain) {
   const KvBatch& k = p.k;
   const int lane = threadIdx.x % kWave;
   long long sum = 0, v = 0, upto = 0;
@@ -125,24 +128,14 @@ __device__ AttnStart attn_start(const AttnArgs& p, int G, int wg, int n_wg, long
     upto += sum;
     sum = lane_of(upto, kWave - 1);
   }
-  if (wg == 0 && __any(bad) && threadIdx.x == 0 && p.dev_err)
+  if (blockIdx.x == 0 && __any(bad) && threadIdx.x == 0 && p.dev_err)
     atomicOr(p.dev_err, GDN_DEV_ERR_LENGTH);
   AttnStart a{};
   a.s.layer = sum;
   a.s.total = sum * p.L;
-  const long long most = static_cast<long long>(n_wg) * grain;
-  a.s.active = a.s.total >= most
-                   ? n_wg
-                   : static_cast<int>((static_cast<double>(a.s.total) + grain - 1) / grain);
-  // a whole number of workgroups per key head, so that with sequences of one
-  // length, or a single one, no part holds the end of one head and the start
-  // of the next
-  const int heads = p.Hkv * p.L;
-  if (heads <= n_wg) {
-    const int up = (a.s.active + heads - 1) / heads * heads;
-    a.s.active = up <= n_wg ? up : n_wg / heads * heads;
-  }
-  a.s.active = uni(a.s.active);
+  a.s.active = uni(attn_active(a.s.total, n_wg, grain, p.Hkv * p.L));
+  const int block = blockIdx.x;
+  const int wg = a.wg = NEAR ? attn_spread(block, a.s.active, kNumXcd) : block;
   if (wg >= a.s.active) return a;
   a.lo = uni(part_of(wg, a.s.total, a.s.active));
   a.hi = uni(part_of(wg + 1, a.s.total, a.s.active));

@@ -274,9 +274,9 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
   const int c = lane % 16, g = lane / 16;
   const int G = p.Hq / p.Hkv;
   const float inv_g = 1.f / static_cast<float>(G);
-  const int wg = blockIdx.x;
   const Places<R, D> places(p.ws, n_wg);
-  const AttnStart st = attn_start<Line>(p, G, wg, n_wg, grain);
+  const AttnStart st = attn_start<Line, false>(p, G, n_wg, grain);
+  const int wg = st.wg;
   AttnJoin join;
   join.last = -1;
   // scores are compared unscaled (a negative scale turns q's sign); at least
@@ -819,13 +819,9 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
   const int c = lane % MR, h = lane / MR;  // row, part
   const int G = p.Hq / p.Hkv;
   const float inv_g = 1.f / static_cast<float>(G);
-  // neighbours on the line share a head's keys: give them one XCD's L2
-  const int wg = n_wg % kNumXcd == 0
-                     ? static_cast<int>(blockIdx.x) % kNumXcd * (n_wg / kNumXcd) +
-                           static_cast<int>(blockIdx.x) / kNumXcd
-                     : static_cast<int>(blockIdx.x);
   const Places<R, D> places(p.ws, n_wg);
-  const AttnStart st = attn_start<Line>(p, G, wg, n_wg, grain);
+  const AttnStart st = attn_start<Line, true>(p, G, n_wg, grain);
+  const int wg = st.wg;
   AttnJoin join;
   join.last = -1;
   const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
