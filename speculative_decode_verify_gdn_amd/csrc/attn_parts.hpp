@@ -6,14 +6,19 @@ namespace gdn {
 
 // Workgroups that take part, of n_wg: a grain of the line's length for each, and a
 // whole number of them per key head, so that with sequences of one length, or a
-// single one, no part holds the end of one head and the start of the next.
-constexpr int attn_active(long long total, int n_wg, long long grain, int heads) {
+// single one, no part holds the end of one head and the start of the next.  Where
+// there are not that many, fewer take part, if at most `idle` are left without work
+// by that (what each kernel gains and loses stands beside its number).
+constexpr int attn_active(long long total, int n_wg, long long grain, int heads, int idle) {
   int active = total >= n_wg * grain
                    ? n_wg
                    : static_cast<int>((static_cast<double>(total) + grain - 1) / grain);
   if (heads <= n_wg) {
     const int up = (active + heads - 1) / heads * heads;
-    active = up <= n_wg ? up : n_wg / heads * heads;
+    if (up <= n_wg)
+      active = up;
+    else if (n_wg % heads <= idle)
+      active = n_wg / heads * heads;
   }
   return active;
 }

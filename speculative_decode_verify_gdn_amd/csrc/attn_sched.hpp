@@ -106,9 +106,9 @@ struct AttnStart {
   KvSpan span;       // of sequence b
 };
 
-// NEAR: neighbours on the line to one XCD.
+// NEAR: neighbours on the line to one XCD.  idle: as attn_active has it.
 template <typename Line, bool NEAR>
-__device__ AttnStart attn_start(const AttnArgs& p, int G, int n_wg, long long grain) {
+__device__ AttnStart attn_start(const AttnArgs& p, int G, int n_wg, long long grain, int idle) {
   const KvBatch& k = p.k;
   const int lane = threadIdx.x % kWave;
   long long sum = 0, v = 0, upto = 0;
@@ -133,7 +133,7 @@ __device__ AttnStart attn_start(const AttnArgs& p, int G, int n_wg, long long gr
   AttnStart a{};
   a.s.layer = sum;
   a.s.total = sum * p.L;
-  a.s.active = uni(attn_active(a.s.total, n_wg, grain, p.Hkv * p.L));
+  a.s.active = uni(attn_active(a.s.total, n_wg, grain, p.Hkv * p.L, idle));
   const int block = blockIdx.x;
   const int wg = a.wg = NEAR ? attn_spread(block, a.s.active, kNumXcd) : block;
   if (wg >= a.s.active) return a;

@@ -432,6 +432,15 @@ def test_attention_layers_of_tiles(T):
     check_attention(R.Batch(95, [40, 300], [T, T - 1], L=5, Hq=8, Hkv=2, D=128))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 6, 20])
+@pytest.mark.parametrize("L", [30, 75])
+def test_attention_heads_that_do_not_divide_the_workgroups(L, T, dtype):
+    """More key heads over the layers than half of the workgroups, and as many as
+    leave a few: workgroups end one head and begin the next, or stay without work."""
+    check_attention(R.Batch(107, [700, 90], [T, T], L=L, Hq=16, Hkv=4, D=64, dtype=dtype, page=64))
+
+
 @pytest.mark.parametrize("T", [3, 9, 60])
 def test_attention_without_tokens(T):
     """No new tokens at all: nothing is written."""
