@@ -204,7 +204,8 @@ def prepare(case, seed):
         s.update(q=(1.5 * torch.randn(1, N, case["Hq"], D, generator=g, device="cuda")).to(dt),
                  o=torch.zeros(1, N, case["Hq"], D, device="cuda", dtype=dt), parent=None)
         if case["tree"]:
-            s["parent"] = _i32(sum(_trees(case, new)[0], []))
+            # one entry for each of the N rows, of no sequence too
+            s["parent"] = _i32(sum(_trees(case, new)[0], []) + [-1] * (N - starts[-1]))
         return s
     slots = [pool["rows"][b][(ctx[b] + i) // page] * page + (ctx[b] + i) % page
              for b in range(case["B"]) for i in range(new[b])]
@@ -247,13 +248,10 @@ def _run_own(s):
         if op == "attend":
             s["workspace"] = torch.empty(gb.attn_verify_workspace_bytes(s["shape"], s["T"], s["N"]),
                                          dtype=torch.uint8, device="cuda")
-            if s["parent"] is not None:  # one entry for each of the N rows, of no sequence too
-                behind = s["N"] - s["parent"].shape[0]
-                s["parents"] = torch.cat([s["parent"], s["parent"].new_full((behind,), -1)])
     sh = s["shape"]
     if op == "attend":
         gb.attn_verify(sh, s["q"], s["seq_len"], s["table"], s["k_cache"], s["v_cache"], s["o"],
-                       s["workspace"], s["T"], q_start=s["q_start"], parent=s.get("parents"),
+                       s["workspace"], s["T"], q_start=s["q_start"], parent=s["parent"],
                        dev_err=s["dev_err"])
         return s["o"]
     if op == "reserve":
@@ -290,7 +288,7 @@ def _attend(s):
     key = torch.arange(S, device="cuda")
     rel = key[None] - ctx[:, None]  # [B,S] place among the new tokens
     if c["tree"]:
-        par = s["parent"].reshape(B, T).long()
+        par = s["parent"][:B * T].reshape(B, T).long()
         step = torch.eye(T, device="cuda", dtype=torch.float64) + (par[:, :, None] == row).double()
         above = torch.linalg.matrix_power(step, T) > 0  # an ancestor, or the node itself
         inside = above.gather(2, rel.clamp(0, T - 1)[:, None, :].expand(B, T, S)) & (rel < new[:, None])[:, None]
