@@ -470,8 +470,9 @@ gdn_status kv_append(const kv_shape* shape, int32_t n_tokens, const void* k, int
  *   workspace   device scratch of attn_verify_workspace_bytes(shape, T,
  *               n_tokens), 16-byte aligned; calls that may overlap need one
  *               each
- * Scores, the softmax's running maximum and sum, and the output sums are fp32;
- * with bf16 the probabilities are rounded to bf16 for the product with V.
+ * Scores, the softmax's running maximum and sum, and the output sums are fp32.
+ * With bf16 and T * Hq/Hkv > 64 the probabilities are rounded to bf16 for the
+ * product with V (2^-8 of each); otherwise they are held to 2^-16 there.
  * Cache places behind a sequence's last token may hold anything, NaN included.
  * So may masked new tokens: an infinite or NaN value (or key) of a token
  * reaches only the rows that attend to it.  It reaches all of those, however

@@ -22,9 +22,17 @@
 // registers and are used once; their bytes bound it.  Many rows in
 // bf16 (k_attn_tile): they pass through LDS, where several waves read them, and
 // the matrix products bound it.  k_attn_join adds up the items that workgroups
-// share.  Rounding: scores, maxima, sums and outputs are fp32; with bf16 each
-// probability is rounded once, as an operand (2^-8 of itself, as the output is
-// again), and the sum l takes it before that.
+// share.
+//
+// Rounding: scores, maxima, sums and outputs are fp32, and the sum l takes every
+// probability as it is.  As an operand beside bf16 values a probability becomes the
+// bf16 nearest to it and, in a second product, the bf16 nearest to what is left
+// (2^-16 of it), so that the output's own rounding is the only one that shows:
+// 0.0017 of the result, as with probabilities in fp32.  The bytes that bound the
+// kernels of up to 64 rows hide nearly all of that (24 long contexts 89.1 and 90.3 us
+// without and with it, drafts 63.6 and 64.0).  Tiles of 128 rows are bound by their
+// products and take the first operand alone, off by 2^-8 of it (0.0023 of the result):
+// with both, the prompts take 850 us instead of 612, the trees 208 instead of 178.
 
 #include <type_traits>
 
@@ -103,14 +111,15 @@ struct Frag<float> {
 
 // O^T += V^T P^T over 32 keys; p[t] holds tile t's probabilities.
 __device__ __forceinline__ floatx4 weigh(const bf16x8* v, const floatx4* p, floatx4 o) {
-  const floatx4 a = p[0], b = p[1];
-  bf16x8 w;
+  bf16x8 w, rest;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = static_cast<__bf16>(a[i]);
-    w[i + 4] = static_cast<__bf16>(b[i]);
+  for (int i = 0; i < 8; ++i) {
+    const float x = p[i / 4][i % 4];
+    w[i] = static_cast<__bf16>(x);
+    rest[i] = static_cast<__bf16>(x - static_cast<float>(w[i]));
   }
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], w, o, 0, 0, 0);
+  o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], w, o, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], rest, o, 0, 0, 0);
 }
 __device__ __forceinline__ floatx4 weigh(const floatx4* v, const floatx4* p, floatx4 o) {
 #pragma unroll
@@ -745,6 +754,7 @@ template <int D, int ROWS>
 struct Tile {
   static constexpr bool kNarrow = ROWS == 64 || D == 256;  // Rows16
   static constexpr int R = ROWS;
+  static constexpr bool kRest = ROWS == 64;  // what a probability's rounding leaves counts too
   // With 256 channels and 64 rows the tile is halved: two workgroups' LDS fit on a CU.
   static constexpr int kKeys = D == 256 && ROWS == 64 ? 32 : 64;
   typedef typename std::conditional<kNarrow, Rows16<D, kKeys>, Rows32<D, kKeys>>::type Mma;
@@ -978,7 +988,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
             });
       };
       // Raises the maximum where it has to, then turns scores into probabilities.
-      auto weights = [&](const Acc* sc, bf16x8* pf) {
+      auto weights = [&](const Acc* sc, bf16x8* pf, bf16x8* rest) {
         float top = sc[0][0];
 #pragma unroll
         for (int t = 0; t < KB; ++t)
@@ -1004,25 +1014,29 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
                 __builtin_amdgcn_exp2f(fmaf(sc[Mm::tile_of(i, e)][Mm::reg_of(i, e)], c2, -at));
             l += w;
             pf[i][e] = static_cast<__bf16>(w);
+            if (Tl::kRest) rest[i][e] = static_cast<__bf16>(w - static_cast<float>(pf[i][e]));
           }
       };
-      auto values = [&](const bf16x8* pf, const u32x4* vl) {
+      auto values = [&](const bf16x8* pf, const bf16x8* rest, const u32x4* vl) {
         products<NG * DT>(
             [&](int n) {
               return __builtin_bit_cast(
                   bf16x8, vl[v_at + n / DT * (Mm::kEvery / 8) * D + n % DT * MR]);
             },
-            [&](int n, bf16x8 vf) { o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]); });
+            [&](int n, bf16x8 vf) {
+              o[n % DT] = Mm::mul(vf, pf[n / DT], o[n % DT]);
+              if (Tl::kRest) o[n % DT] = Mm::mul(vf, rest[n / DT], o[n % DT]);
+            });
       };
       // A tile that every row sees all of.
       auto plain = [&](const u32x4* kl) {
         const u32x4* const vl = kl + KT * P;
         if (any_sees == 0) return;  // a wave without rows
         Acc sc[KB];
-        bf16x8 pf[NG];
+        bf16x8 pf[NG], rest[NG];
         scores(sc, kl);
-        weights(sc, pf);
-        values(pf, vl);
+        weights(sc, pf, rest);
+        values(pf, rest, vl);
       };
       // A tile with keys that some row does not see or that are not there.
       // Values that are not there, infinities and NaN are left out, as in the
@@ -1048,7 +1062,7 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
         lds_barrier();
         if (kb >= any_sees) return;
         Acc sc[KB];
-        bf16x8 pf[NG];
+        bf16x8 pf[NG], rest[NG];
         scores(sc, kl);
         // the first of the lane's eight keys of group i, and those of them that are there
         auto base_of = [&](int i) { return kb + Mm::kEvery * i + opaque(8 * h); };
@@ -1067,8 +1081,8 @@ __global__ __launch_bounds__((Tile<D, ROWS>::W * kWave), 2) void k_attn_tile(Att
             sc[Mm::tile_of(i, e)][Mm::reg_of(i, e)] = (sees >> e) & 1 ? z : kNegInf;
           }
         }
-        weights(sc, pf);
-        values(pf, vl);
+        weights(sc, pf, rest);
+        values(pf, rest, vl);
       };
 
       lds_loads_done();

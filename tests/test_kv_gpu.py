@@ -1,5 +1,7 @@
 """The paged key/value cache calls and the attention over it, on the GPU,
 against the plain 64-bit implementations."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -245,6 +247,24 @@ def test_attention_masked_tokens_hold_nan_and_infinities(tree, T, dtype):
     tol = np.where(np.isfinite(want), tol, 0.0)
     close(got, want, tol, "o")
     assert np.isnan(want).any() and np.isinf(want).any() and np.isfinite(want).any()
+
+
+@pytest.mark.parametrize("Hq,T", [(8, 1), (16, 2), (16, 4), (32, 4), (2, 8), (4, 32), (2, 64)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_probabilities_of_16_bits_lose_nothing(D, Hq, T):
+    """bf16 with at most 64 query rows to a key head: a probability is held to 2^-16
+    for the product with V, so that beside fp32's own errors only the output's rounding
+    counts.  tol: fp32's, then 2^-16 of sum p |v|, which is at most the largest |v|,
+    then 2^-8 of the result as it stands before the last rounding."""
+    bt = R.Batch(108, [9, 300, 2000], [T, T, max(1, T - 1)], Hq=Hq, Hkv=2, D=D, page=64)
+    table, slots, _ = check_reserve(bt)
+    bt.g_append()
+    kc, vc, _ = bt.r_append(slots)
+    bt.g_attend()
+    bt.sh = dataclasses.replace(bt.sh, dtype=F32)  # of the plain form: its tolerance in fp32
+    want, tol = bt.r_attend(table, kc, vc)
+    tol = tol + 2.0 ** -16 * np.abs(vc).max()
+    close(R.hostf(bt.d["o"]).astype(np.float64), want, tol + 2.0 ** -8 * (np.abs(want) + tol), "o")
 
 
 def test_attention_strided_q():
