@@ -1367,13 +1367,13 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p, int n_wg) {
   }
 }
 
-// A workgroup has at least this many keys' cost.  Stream kernel in bf16 256 (one
-// sequence of 800 tokens: level with 128); in 32 bits, where a key's products take
-// sixteen times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64.
-// Tile kernel: one tree of 64 nodes behind 2,000 tokens 38 us with 256, 35 with 128,
-// 34.5 with 96; two prompts of 1,000 tokens and 6 heads 44, 42.5 and 42.8.
+// A workgroup has at least this many keys' cost.  In bf16 256: for the stream kernel
+// level with 128 (one sequence of 800 tokens); for the tile kernel 8 drafts behind
+// 16,000 tokens take 24.1 us with 256, 28.2 with 192, 29.4 with 128, a prompt of 300
+// tokens 29, 32 and 38, 4 sequences of 8 drafts 20.4, 19.9 and 24.2, 8 drafts behind
+// 1,000 tokens 17.5, 16.6 and 16.0.  In 32 bits, where a key's products take sixteen
+// times as long, fewer: 90 rows of three heads 47 us with 256, 24 with 64.
 constexpr long long grain_of(int size) { return size == 2 ? 256 : 64; }
-constexpr long long kTileGrain = 128;
 constexpr int kCus = 256;
 static_assert(2 * kCus <= kMostWg, "the join counts no more");
 
@@ -1424,7 +1424,7 @@ hipError_t stream_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 template <int D, int ROWS>
 hipError_t tile_t(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  k_attn_tile<D, ROWS><<<p.wgs, Tile<D, ROWS>::W * kWave, 0, s>>>(a, p.wgs, kTileGrain);
+  k_attn_tile<D, ROWS><<<p.wgs, Tile<D, ROWS>::W * kWave, 0, s>>>(a, p.wgs, grain_of(2));
   return join_t<uint16_t, D, ROWS>(a, p.wgs, s);
 }
 
