@@ -673,9 +673,12 @@ __global__ __launch_bounds__(256, 1) void k_attn_stream(AttnArgs p, int n_wg, lo
 // itself: 289 against 235 us for 64 trees of 64 nodes, 16 query heads).
 //
 // Three prompts of about 3,000 tokens behind 1,000 cached ones, 32 query heads of
-// 128 channels: 600 us, 900 TFLOP/s; a large matrix product reaches 1,189.  The
-// rest is the vector work of the softmax, which the matrix pipe hides in part.
-// 64-row tiles of 32 drafted chunks: 52 us for 198 MB; the bytes alone take 41.
+// 128 channels: 580 to 640 us by card, 930 to 840 TFLOP/s; a large matrix product
+// reaches 1,189.  The rest is the vector work of the softmax, which the matrix pipe
+// hides in part.  64-row tiles of 32 drafted chunks: 54 us for 198 MB; the bytes alone
+// take 41.  64 trees of 512 rows to a key head of 256 channels: 160 us and more, for
+// which four tiles sweep the same keys, in turn and from memory: 6.0e6 L2 misses, 765
+// MB in lines of 128 bytes, for 254 MB of operands.
 //
 // LDS: keys row by row, 16-byte pieces of a row permuted by the key so that the
 // rows that are read together fall on different banks; values as in the cache,
@@ -1378,7 +1381,8 @@ constexpr int kCus = 256;
 static_assert(2 * kCus <= kMostWg, "the join counts no more");
 
 // The kernel and tile for sequences of at most `rows` query rows, and how many
-// workgroups: as many as the chip holds at once.
+// workgroups: two to a CU, or one where LDS or registers hold no second.  (With 64
+// channels in bf16 three or four would fit; the join counts no more than 512.)
 struct AttnPlan {
   int tile;  // rows of the tile kernel's tile, or 0: the stream kernel
   int nt;    // its 16s of rows
@@ -1387,12 +1391,13 @@ struct AttnPlan {
 };
 
 // Rows of the stream kernel's tile in 16s: with bf16 it takes 16 rows at most, and
-// the tile kernel more (64 rows of 32 sequences of about 3,000 keys: 44 us there, 74
-// us with 64 rows' sums in one wave's registers).  In 32 bits 32 rows, as far as
-// their sums stay in registers beside the operands.
+// the tile kernel more (32 rounds of 64 rows and about 3,000 keys: 92 us by the stream
+// kernel with 64 rows' sums in one wave's registers, 68 by tiles when they were taken).
+// In 32 bits 32 rows; with 256 channels 16, whose sums and operands already spill 140
+// bytes a lane.
 constexpr int stream_most(int head_dim, int size) { return size == 2 || head_dim == 256 ? 1 : 2; }
 AttnPlan attn_plan(long long rows, int head_dim, int size) {
-    AttnPlan a{0, 1, 2 * kCus};
+  AttnPlan a{0, 1, 2 * kCus};
   if (size == 2 && rows > 16) {
     a.tile = rows > 64 ? 128 : 64;
     // LDS for one workgroup on a CU (64 trees: 186 us; two parts for each 202)

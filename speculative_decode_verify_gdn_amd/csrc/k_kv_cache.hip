@@ -220,8 +220,9 @@ __global__ __launch_bounds__(kNT) void k_kv_append(KvAppendArgs p) {
 // A row of k is a few 16-byte pieces, a lane each.  A row of v lies in the cache with
 // 8 slots between two channels, so neighbouring lanes take neighbouring channels
 // and a store touches as few lines as it can (64 trees over ten layers: 29 us with
-// 16-byte pieces of v, 25 so, 12 with the pages dealt out as below; latency again:
-// 12 MB move, and the path, its slots and its rows are loads that wait for each other).
+// 16-byte pieces of v, 25 so, 12 with the pages dealt out as below.  The copies of 12
+// MB take those 12 by themselves, the counts 5: loads of the path, its slots and its
+// rows that wait for each other, and 2-byte stores 16 bytes apart).
 template <typename T, int D>
 __device__ void commit_rows(const KvCommitArgs& p, int b, int l) {
   constexpr int E = 16 / sizeof(T);   // elements of a piece
