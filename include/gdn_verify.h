@@ -491,7 +491,8 @@ gdn_status attn_verify(const kv_shape* shape, int32_t T, int32_t n_tokens, const
                        const void* v_cache, void* o, void* workspace, size_t workspace_bytes,
                        int32_t* dev_err, void* stream);
 
-/* Bytes of device workspace attn_verify needs (0 for arguments it refuses). */
+/* Bytes of device workspace attn_verify needs (0 for arguments it refuses).  They
+ * do not fall with T, so a workspace made for the largest T serves smaller ones. */
 size_t attn_verify_workspace_bytes(const kv_shape* shape, int32_t T, int32_t n_tokens);
 
 /*

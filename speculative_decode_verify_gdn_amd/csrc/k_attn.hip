@@ -1463,9 +1463,17 @@ hipError_t launch_attn(const AttnArgs& a, int head_dim, int dtype, hipStream_t s
   return hipErrorInvalidValue;
 }
 
+// The most that any call of as many rows or fewer needs: narrow tiles on more
+// workgroups can take a little more than wide ones on fewer.
 size_t attn_workspace(long long rows, int head_dim, int dtype) {
-  const AttnPlan p = attn_plan(rows, head_dim, dtype == 1 ? 2 : 4);
-  return places_bytes(p.rows(), head_dim, p.wgs);
+  size_t most = 0;
+  for (long long r : {1LL, 17LL, 65LL}) {  // the least rows of each plan
+    if (r > rows) break;
+    const AttnPlan p = attn_plan(r, head_dim, dtype == 1 ? 2 : 4);
+    const size_t bytes = places_bytes(p.rows(), head_dim, p.wgs);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 }  // namespace gdn

@@ -124,6 +124,17 @@ def test_attention_refusals(lib):
     assert lib.attn_verify_workspace_bytes(shape(), 4, 0) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_workspace_does_not_fall_with_the_tokens(lib, D, dtype):
+    """A workspace made for the largest T, batch and n_tokens serves smaller calls."""
+    for Hq in (1, 4, 7, 16, 70):
+        sh = shape(Hq=Hq, Hkv=1, D=D, dtype=dtype)
+        got = [lib.attn_verify_workspace_bytes(sh, T, 2 * T) for T in range(1, 300)]
+        assert got[0] > 0 and all(a <= b for a, b in zip(got, got[1:]))
+        assert got[-1] == lib.attn_verify_workspace_bytes(sh, 299, 10000)
+
+
 def test_commit_refusals(lib):
     good = [shape(), 4, 8, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 128,
             FAKE, 128, FAKE, FAKE, None, None]
